@@ -236,6 +236,154 @@ int tlsp_pooled_block_select(const tlsp_dims* dims, const void* Q, const void* K
                              int32_t* indices, float* block_scores, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions. A pair of channels (x1, x2) of a token at position p is
+ * turned by the angle a = p * w, w being the pair's frequency:
+ *   y1 = A (x1 cos a - x2 sin a),   y2 = A (x2 cos a + x1 sin a).
+ * The first rotary_dim channels of each head are turned; the others pass.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+  TLSP_ROTARY_HALF = 0,        /* pair i: channels i and i + rotary_dim / 2 */
+  TLSP_ROTARY_INTERLEAVED = 1  /* pair i: channels 2i and 2i + 1 */
+} tlsp_rotary_layout;
+
+typedef enum {
+  TLSP_ROTARY_NONE = 0,
+  TLSP_ROTARY_LINEAR = 1, /* w / factor */
+  TLSP_ROTARY_BASE = 2,   /* base * factor^(D / (D - 2)), D = 2 * the section's pairs (D > 2) */
+  TLSP_ROTARY_RAMP = 3    /* c w + (1 - c) w / factor with
+                             c = clamp((original_len w / 2 pi - slow) / (fast - slow), 0, 1) */
+} tlsp_rotary_scaling;
+
+#define TLSP_ROTARY_MAX_PAIRS 128
+#define TLSP_ROTARY_MAX_AXES 4
+
+typedef struct {
+  int32_t head_dim;   /* multiple of 8, 8 .. 256 */
+  int32_t rotary_dim; /* even, 2 .. head_dim */
+  tlsp_rotary_layout layout;
+  int32_t axes;                            /* 1 .. TLSP_ROTARY_MAX_AXES position axes */
+  int32_t sections[TLSP_ROTARY_MAX_AXES];  /* consecutive pairs per axis; sum = rotary_dim / 2 */
+  tlsp_rotary_scaling scaling;
+  double base;          /* pair i of a section of s pairs: w = base^(-i / s) */
+  double factor;        /* >= 1 */
+  double original_len;  /* TLSP_ROTARY_RAMP: > 0 */
+  double fast, slow;    /* TLSP_ROTARY_RAMP: turns over original_len, fast > slow >= 0 */
+  double amplitude;     /* A (> 0), or 0: 1 + 0.1 ln(factor) with TLSP_ROTARY_RAMP, else 1 */
+} tlsp_rotary_desc;
+
+/* What a call needs of a description, on the host; made once, passed by value
+ * to every call. `turns` holds w / 2 pi modulo 1 as a 64-bit fraction, so the
+ * angle of any 64-bit position is reduced exactly (the product wraps). */
+typedef struct {
+  int32_t head_dim, rotary_dim, layout, axes;
+  float amplitude;
+  int32_t reserved;
+  uint8_t axis[TLSP_ROTARY_MAX_PAIRS];
+  uint64_t turns[TLSP_ROTARY_MAX_PAIRS];
+} tlsp_rotary_plan;
+
+int tlsp_rotary_make_plan(const tlsp_rotary_desc* desc, tlsp_rotary_plan* plan);
+
+/* A tensor [batch, tokens, heads, head_dim] in any order of its first three
+ * axes: strides in elements, channels contiguous. */
+typedef struct {
+  const void* in;
+  void* out; /* may be `in` itself with the same strides (in place); no other overlap */
+  int64_t in_batch, in_token, in_head;
+  int64_t out_batch, out_token, out_head;
+  int32_t heads;
+} tlsp_rotary_tensor;
+
+typedef struct {
+  int32_t batch, tokens;
+  tlsp_dtype dtype;
+  int32_t positions_64;                /* 0: int32 positions, 1: int64 */
+  const void* positions;               /* [axes, batch or 1, tokens] with the strides below */
+  int64_t position_axis, position_batch; /* strides in elements (tokens contiguous) */
+} tlsp_rotary_call;
+
+/* Rotates one or two tensors (queries and keys; `K` may be NULL) of the same
+ * tokens in one launch. backward = 1 applies the transposed map, which turns
+ * the gradient of y into the gradient of x. Pointers and strides need only
+ * the alignment of the element; 16-byte aligned rows are read 16 bytes at a
+ * time. fp32 arithmetic, one rounding to the output type. */
+int tlsp_rotary(const tlsp_rotary_plan* plan, const tlsp_rotary_call* call,
+                const tlsp_rotary_tensor* Q, const tlsp_rotary_tensor* K, int32_t backward,
+                void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over packed sequences. The sequences of a batch lie end to end
+ * along the token axis of Q, O [tokens, heads, d] and K, V [tokens, kv_heads,
+ * d]; query head h reads key/value head h / (heads / kv_heads). With `causal`,
+ * query i of a sequence of n queries and m keys sees its keys j <= i + m - n
+ * (the last query sees every key); else all m. With a shared prefix, every
+ * query of every sequence also sees all prefix_len prefix keys. A row that
+ * sees no key has O = 0 and log partition -inf. A key that a row does not see
+ * has no influence on it, whatever its K and V hold.
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  int32_t num_seqs;   /* >= 1 */
+  int32_t heads;      /* a multiple of kv_heads, heads / kv_heads <= 64 */
+  int32_t kv_heads;   /* >= 1 */
+  int32_t head_dim;   /* 64 or 128 */
+  tlsp_dtype dtype;
+  int32_t causal;     /* 0 or 1 */
+  int32_t prefix_len; /* >= 0 */
+} tlsp_packed_desc;
+
+/* The work of one batch, laid out on the host from its lengths: made once
+ * per batch, used by every layer. */
+typedef struct {
+  tlsp_packed_desc desc;
+  int32_t tile_items, token_items, merge_items, reserved;
+  int64_t q_rows;      /* query tokens of all sequences */
+  int64_t kv_rows;     /* rows K and V must have (the furthest key + 1) */
+  int64_t part_rows;   /* query tokens x key ranges whose partial results are merged */
+  uint64_t items_bytes; /* size of the item table (host buffer, then device copy) */
+  uint64_t ws_bytes;    /* workspace of a call */
+} tlsp_packed_plan;
+
+/* Fills `plan` and, if items_bytes is large enough, the item table `items`
+ * (host memory; the caller copies plan->items_bytes bytes of it to the
+ * device). TLSP_ERR_WORKSPACE: items_bytes is too small (items may then be
+ * NULL); plan->items_bytes is what is needed.
+ *   q_lens, kv_lens   [num_seqs], each >= 0, on the host.
+ *   kv_starts         [num_seqs] first key row of each sequence (for caches
+ *                     with room behind each sequence), or NULL: end to end. */
+int tlsp_packed_make_plan(const tlsp_packed_desc* desc, const int32_t* q_lens,
+                          const int32_t* kv_lens, const int64_t* kv_starts, void* items,
+                          size_t items_bytes, tlsp_packed_plan* plan);
+
+/* A tensor [tokens, heads, d]: strides in elements (multiples of 16 bytes),
+ * channels contiguous, 16-byte aligned base. */
+typedef struct {
+  void* ptr;
+  int64_t row_stride, head_stride;
+} tlsp_rows;
+
+/* O (and lse fp32 [q_rows, heads], natural log, if not NULL) of the packed
+ * sequences of a plan without prefix. `items` is the device copy of the item
+ * table (16-byte aligned). scale multiplies q . k (0: 1/sqrt(d)). Rows of O
+ * and lse behind the last sequence are not written. ws: at least
+ * plan->ws_bytes, zero-filled once before its first use; calls that may
+ * overlap in time need workspaces of their own. */
+int tlsp_packed_attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* Q,
+                          const tlsp_rows* K, const tlsp_rows* V, const tlsp_rows* O, float* lse,
+                          float scale, void* ws, size_t ws_bytes, void* stream);
+
+/* The same for a plan with prefix_len > 0: Kp, Vp [prefix_len, kv_heads, d].
+ * The prefix is read once for all sequences with few queries each: their
+ * rows share its key tiles, and the partial results over prefix and own keys
+ * are merged by their log partitions. K and V may be NULL when no sequence
+ * has keys of its own. */
+int tlsp_prefix_attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* Q,
+                          const tlsp_rows* Kp, const tlsp_rows* Vp, const tlsp_rows* K,
+                          const tlsp_rows* V, const tlsp_rows* O, float* lse, float scale,
+                          void* ws, size_t ws_bytes, void* stream);
+
 /* Device status recorded in `ws` (TLSP_OK, TLSP_ERR_TIMEOUT or
  * TLSP_ERR_DEVICE_ASSERT). Synchronises with the device (blocking copy of the
  * status word): call it after the stream that used `ws` has finished. */

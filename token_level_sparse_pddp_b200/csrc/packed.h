@@ -1,0 +1,68 @@
+// Shared between the planner of the packed attention calls (packed_plan.cu)
+// and their kernels.
+#pragma once
+
+#include "kernels.h"
+
+namespace tlsp {
+
+// Query tokens q0 .. q0 + nt - 1 (all query heads of one key/value head)
+// against prefix keys pre0 .. pre0 + pre_n - 1, which every token sees, and
+// the key rows kv0 .. kv0 + kv_n - 1 of K, of which token q0 + i sees the first
+// min(kv_n, diag + i + 1) (none if that is negative).
+// slot < 0: the result is final; else it is the partial result of token
+// q0 + i in row slot + i of the workspace's partial rows.
+struct PackedItem {
+  int32_t q0, nt;
+  int32_t kv0, kv_n;
+  int32_t pre0, pre_n;
+  int32_t diag, slot;
+};
+static_assert(sizeof(PackedItem) == 32, "item table layout");
+
+// Tokens q0 .. q0 + nt - 1: partial rows a_slot + p * a_stride + i for p <
+// a_parts, then the same with b.
+struct MergeItem {
+  int32_t q0, nt;
+  int32_t a_slot, a_parts, a_stride;
+  int32_t b_slot, b_parts, b_stride;
+};
+static_assert(sizeof(MergeItem) == 32, "item table layout");
+
+constexpr int kTokenRows = 16;    // rows (tokens x heads of a group) of a token item
+constexpr int kSimtTileRows = 64;  // rows of a tile item, fp32
+constexpr int kMergeTokens = 4;   // tokens of a merge item
+
+// Tokens of one tile: whole groups of `group` rows in `rows` rows.
+inline int tile_tokens(int rows, int group) { return rows / group; }
+
+struct PackedArgs {
+  const PackedItem* tiles;
+  const PackedItem* tokens;
+  const MergeItem* merges;
+  int n_tiles, n_tokens, n_merges;
+  int heads, kv_heads, group, d;
+  int64_t q_rows, kv_rows, prefix_len, part_rows;
+  tlsp_rows Q, K, V, Kp, Vp, O;
+  float* lse;       // [q_rows, heads] or null
+  float scale;
+  float* part_lse;  // [part_rows, heads] natural log
+  float* part_o;    // [part_rows, heads, d], normalised
+  int* status;
+};
+
+// An item read from device memory lies within the call's tensors and `rows` rows
+// of a tile (else the caller's table is not the plan's: the item is skipped).
+__device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t, int rows) {
+  const bool pieces = t.nt >= 1 && t.nt * a.group <= rows && t.q0 >= 0 && t.kv0 >= 0 &&
+                      t.kv_n >= 0 && t.pre0 >= 0 && t.pre_n >= 0;
+  return pieces && (int64_t)t.q0 + t.nt <= a.q_rows &&
+         (t.kv_n == 0 || (int64_t)t.kv0 + t.kv_n <= a.kv_rows) &&
+         (int64_t)t.pre0 + t.pre_n <= a.prefix_len && t.diag >= -0x40000000 &&
+         t.diag <= t.kv_n && (t.slot < 0 || (int64_t)t.slot + t.nt <= a.part_rows);
+}
+
+int packed_simt(const PackedArgs& a, bool bf16, cudaStream_t st);
+int packed_merge(const PackedArgs& a, bool bf16, cudaStream_t st);
+
+}  // namespace tlsp

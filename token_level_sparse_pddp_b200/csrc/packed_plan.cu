@@ -1,0 +1,471 @@
+// Packed attention calls: the planner (host) and the entry points.
+//
+// The planner turns the lengths of a batch into a table of work items, so the
+// kernels' grids, the split of long key ranges over CTAs and the merge of
+// their partial results are all settled on the host, once per batch.
+//   tile items   up to a tile's rows of one sequence against its keys (and the
+//                prefix), or the rows of many short sequences against the
+//                prefix, which is then read once for all of them;
+//   token items  up to 16 rows (a few tokens of one sequence) against a range
+//                of keys: memory-bound, split until the GPU is full;
+//   merge items  tokens whose keys were split.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <queue>
+#include <vector>
+
+#include "packed.h"
+
+namespace tlsp {
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr size_t kStatusBytes = 256;
+constexpr int kSms = 148;  // planning assumes a B200
+constexpr int kChunk = 128;  // keys a tile item takes at a time
+
+int validate_desc(const tlsp_packed_desc* d) {
+  if (!d) return TLSP_ERR_INVALID_ARG;
+  if (d->num_seqs < 1 || d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads)
+    return TLSP_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return TLSP_ERR_INVALID_ARG;
+  if (d->dtype != TLSP_F32 && d->dtype != TLSP_BF16) return TLSP_ERR_INVALID_ARG;
+  if ((d->causal != 0 && d->causal != 1) || d->prefix_len < 0) return TLSP_ERR_INVALID_ARG;
+  if (d->heads / d->kv_heads > 64 || d->kv_heads > 65535) return TLSP_ERR_UNSUPPORTED;
+  return TLSP_OK;
+}
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+struct WsLayout {
+  size_t lse, o, total;
+};
+WsLayout ws_layout(const tlsp_packed_plan& p) {
+  WsLayout L{};
+  L.lse = kStatusBytes;
+  L.o = align_up(L.lse + sizeof(float) * (size_t)p.part_rows * p.desc.heads);
+  L.total = align_up(L.o + sizeof(float) * (size_t)p.part_rows * p.desc.heads * p.desc.head_dim);
+  return L;
+}
+
+// Chunks of 128 keys a tile item steps through.
+int64_t steps_of(const PackedItem& t) {
+  return ceil_div(t.pre_n, kChunk) + ceil_div(t.kv_n, kChunk);
+}
+
+// Time of the tile items, in steps, on kSms CTAs taking them longest first,
+// when none may exceed `most` steps; `fixed` steps are charged per item for
+// its prologue and epilogue, as many again for a part's merge.
+double makespan(const std::vector<int64_t>& steps, int kv_heads, int64_t most, double fixed) {
+  std::vector<double> jobs;
+  for (int64_t s : steps) {
+    const int64_t parts = std::max<int64_t>(1, ceil_div(s, most));
+    for (int64_t i = 0; i < parts; ++i)
+      for (int h = 0; h < kv_heads; ++h)
+        jobs.push_back((double)(s * (i + 1) / parts - s * i / parts) + fixed * (parts > 1 ? 2 : 1));
+  }
+  std::sort(jobs.begin(), jobs.end(), std::greater<double>());
+  std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
+  double last = 0;
+  for (double j : jobs) {
+    double at = 0;
+    if ((int)ends.size() == kSms) {
+      at = ends.top();
+      ends.pop();
+    }
+    ends.push(at + j);
+    last = std::max(last, at + j);
+  }
+  return last;
+}
+
+class Planner {
+ public:
+  Planner(const tlsp_packed_desc& d, const int32_t* q_lens, const int32_t* kv_lens,
+          const int64_t* kv_starts)
+      : d_(d), q_lens_(q_lens), kv_lens_(kv_lens), kv_starts_(kv_starts) {
+    group_ = d.heads / d.kv_heads;
+    tile_tokens_ = tile_tokens(kSimtTileRows, group_);
+  }
+
+  int run() {
+    TLSP_TRY(place());
+    // Tile items first; those left whole, then those split.
+    std::vector<PackedItem> whole;
+    for (int s = 0; s < d_.num_seqs; ++s)
+      if (!few_[s])
+        for (int t0 = 0; t0 < q_lens_[s]; t0 += tile_tokens_) whole.push_back(own_tile(s, t0));
+    std::vector<PackedItem> shared;  // rows of few-query sequences against the prefix
+    if (d_.prefix_len > 0) {
+      for (int s = 0; s < d_.num_seqs;) {
+        if (!few_[s]) {
+          ++s;
+          continue;
+        }
+        int e = s;  // a run of such sequences: their queries are consecutive
+        while (e < d_.num_seqs && few_[e]) ++e;
+        const int64_t q0 = q0_[s], n = q0_[e - 1] + q_lens_[e - 1] - q0;
+        const int64_t tiles = ceil_div(n, tile_tokens_);
+        for (int64_t i = 0; i < tiles; ++i) {  // equal shares
+          const int64_t a = n * i / tiles, b = n * (i + 1) / tiles;
+          shared.push_back({(int32_t)(q0 + a), (int32_t)(b - a), 0, 0, 0, d_.prefix_len, 0, 0});
+        }
+        s = e;
+      }
+    }
+    // prefix work of at most kTokenRows rows goes to the token kernel
+    std::vector<PackedItem> shared_tokens;
+    for (size_t i = 0; i < shared.size();) {
+      if (shared[i].nt * group_ <= kTokenRows) {
+        shared_tokens.push_back(shared[i]);
+        shared.erase(shared.begin() + (std::ptrdiff_t)i);
+      } else {
+        ++i;
+      }
+    }
+    const int64_t most = tile_split(whole, shared);
+    for (const PackedItem& t : whole) {
+      const int64_t parts = std::max<int64_t>(1, ceil_div(steps_of(t), most));
+      if (parts == 1) {
+        tiles.push_back(t);
+        continue;
+      }
+      const int64_t base = take_slots(parts * t.nt);
+      split(t, parts, base, tiles);
+      add_merge(t.q0, t.nt, base, parts, t.nt, 0, 0, 0);
+    }
+    // Few-query sequences: own keys in token items, split over the GPU.
+    const int64_t range = token_range(shared_tokens);
+    std::vector<Piece> pieces;  // where the prefix results of each token lie
+    auto add_shared = [&](const PackedItem& t, int64_t parts, std::vector<PackedItem>& to) {
+      const int64_t base = take_slots(parts * t.nt);
+      split(t, parts, base, to);
+      pieces.push_back({t.q0, t.nt, base, parts});
+    };
+    for (const PackedItem& t : shared)
+      add_shared(t, std::max<int64_t>(1, ceil_div(steps_of(t), most)), tiles);
+    for (const PackedItem& t : shared_tokens)
+      add_shared(t, std::max<int64_t>(1, ceil_div(t.pre_n, range)), tokens);
+    std::sort(pieces.begin(), pieces.end(),
+              [](const Piece& a, const Piece& b) { return a.q0 < b.q0; });
+    size_t at = 0;
+    for (int s = 0; s < d_.num_seqs; ++s) {
+      if (!few_[s] || q_lens_[s] == 0) continue;
+      const int32_t n = q_lens_[s], m = kv_lens_[s];
+      const int64_t diag = d_.causal ? (int64_t)m - n : m;
+      const int64_t parts = d_.prefix_len > 0 && m == 0 ? 0 : std::max<int64_t>(1, ceil_div(m, range));
+      const PackedItem t = {(int32_t)q0_[s], n, (int32_t)kv0_[s], m, 0, 0, clamp_diag(diag, m), -1};
+      if (parts == 1 && d_.prefix_len == 0) {
+        tokens.push_back(t);
+        continue;
+      }
+      const int64_t base = take_slots(parts * n);
+      if (parts > 0) split(t, parts, base, tokens);
+      if (d_.prefix_len == 0) {
+        add_merge(t.q0, n, base, parts, n, 0, 0, 0);
+        continue;
+      }
+      int64_t q = q0_[s];
+      while (q < q0_[s] + n) {  // the pieces that hold its prefix results
+        while (pieces[at].q0 + pieces[at].nt <= q) ++at;
+        const Piece& p = pieces[at];
+        const int64_t to = std::min<int64_t>(q0_[s] + n, p.q0 + p.nt);
+        add_merge(q, to - q, p.slot + (q - p.q0), p.parts, p.nt, base + (q - q0_[s]), parts, n);
+        q = to;
+      }
+    }
+    if (part_rows_ > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
+    // longest first: the grid is handed out in this order
+    auto longer = [](const PackedItem& a, const PackedItem& b) {
+      return steps_of(a) > steps_of(b);
+    };
+    std::stable_sort(tiles.begin(), tiles.end(), longer);
+    std::stable_sort(tokens.begin(), tokens.end(), longer);
+    const int64_t most_items =
+        std::max({tiles.size(), tokens.size(), merges.size()}) * (uint64_t)d_.kv_heads;
+    if (most_items > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
+    return TLSP_OK;
+  }
+
+  std::vector<PackedItem> tiles, tokens;
+  std::vector<MergeItem> merges;
+  int64_t q_rows = 0, kv_rows = 0;
+  int64_t part_rows() const { return part_rows_; }
+
+ private:
+  struct Piece {
+    int64_t q0, nt, slot, parts;
+  };
+
+  int place() {
+    q0_.resize(d_.num_seqs);
+    kv0_.resize(d_.num_seqs);
+    few_.resize(d_.num_seqs);
+    int64_t end = 0;
+    for (int s = 0; s < d_.num_seqs; ++s) {
+      const int32_t n = q_lens_[s], m = kv_lens_[s];
+      if (n < 0 || m < 0) return TLSP_ERR_INVALID_ARG;
+      q0_[s] = q_rows;
+      kv0_[s] = kv_starts_ ? kv_starts_[s] : end;
+      if (kv0_[s] < 0) return TLSP_ERR_INVALID_ARG;
+      end += m;
+      q_rows += n;
+      if (m > 0) kv_rows = std::max(kv_rows, kv0_[s] + m);
+      if (m == 0) kv0_[s] = 0;
+      few_[s] = (int64_t)n * group_ <= kTokenRows;
+    }
+    // kernels index tokens with 32 bits (element offsets with 64)
+    if (q_rows > 0x7ffffeffLL || kv_rows > 0x7ffffeffLL) return TLSP_ERR_UNSUPPORTED;
+    return TLSP_OK;
+  }
+
+  static int32_t clamp_diag(int64_t diag, int64_t kv_n) {
+    return (int32_t)std::max<int64_t>(-0x40000000LL, std::min<int64_t>(diag, kv_n));
+  }
+
+  // Tile of the sequence's tokens from t0, with the keys that any of them sees.
+  PackedItem own_tile(int s, int t0) const {
+    const int64_t n = q_lens_[s], m = kv_lens_[s];
+    const int64_t nt = std::min<int64_t>(tile_tokens_, n - t0);
+    const int64_t diag = d_.causal ? m - n + t0 : m;
+    const int64_t keys = std::max<int64_t>(0, std::min<int64_t>(m, diag + nt));
+    return {(int32_t)(q0_[s] + t0), (int32_t)nt, (int32_t)kv0_[s], (int32_t)keys,
+            0, d_.prefix_len, clamp_diag(diag, m), -1};
+  }
+
+  // Cuts an item's keys (prefix, then own) at whole chunks into `parts`.
+  void split(const PackedItem& t, int64_t parts, int64_t base, std::vector<PackedItem>& to) {
+    const int64_t pre_steps = ceil_div(t.pre_n, kChunk), steps = steps_of(t);
+    for (int64_t p = 0; p < parts; ++p) {
+      const int64_t a = steps * p / parts, b = steps * (p + 1) / parts;
+      PackedItem x = t;
+      const int64_t pa = std::min(a, pre_steps) * kChunk, pb = std::min(b, pre_steps) * kChunk;
+      x.pre0 = (int32_t)(t.pre0 + std::min<int64_t>(pa, t.pre_n));
+      x.pre_n = (int32_t)(std::min<int64_t>(pb, t.pre_n) - std::min<int64_t>(pa, t.pre_n));
+      const int64_t oa = std::max<int64_t>(0, a - pre_steps) * kChunk;
+      const int64_t ob = std::max<int64_t>(0, b - pre_steps) * kChunk;
+      x.kv0 = (int32_t)(t.kv0 + std::min<int64_t>(oa, t.kv_n));
+      x.kv_n = (int32_t)(std::min<int64_t>(ob, t.kv_n) - std::min<int64_t>(oa, t.kv_n));
+      x.diag = clamp_diag((int64_t)t.diag - oa, x.kv_n);
+      x.slot = (int32_t)(base + p * t.nt);
+      to.push_back(x);
+    }
+  }
+
+  int64_t take_slots(int64_t n) {
+    const int64_t at = part_rows_;
+    part_rows_ += n;
+    return at;
+  }
+
+  void add_merge(int64_t q0, int64_t n, int64_t a, int64_t a_parts, int64_t a_stride, int64_t b,
+                 int64_t b_parts, int64_t b_stride) {
+    for (int64_t i = 0; i < n; i += kMergeTokens)
+      merges.push_back({(int32_t)(q0 + i), (int32_t)std::min<int64_t>(kMergeTokens, n - i),
+                        (int32_t)(a + i), (int32_t)a_parts, (int32_t)a_stride, (int32_t)(b + i),
+                        (int32_t)b_parts, (int32_t)b_stride});
+  }
+
+  // Most steps of a tile item. With many more items than SMs they stay whole;
+  // else the split of least estimated time is taken.
+  int64_t tile_split(const std::vector<PackedItem>& whole, const std::vector<PackedItem>& shared) {
+    std::vector<int64_t> steps;
+    int64_t total = 0, longest = 1;
+    for (const auto* v : {&whole, &shared})
+      for (const PackedItem& t : *v) {
+        steps.push_back(steps_of(t));
+        total += steps.back();
+        longest = std::max(longest, steps.back());
+      }
+    if (steps.empty()) return 1;
+    const int64_t jobs = (int64_t)steps.size() * d_.kv_heads;
+    const double mean = (double)total * d_.kv_heads / kSms;
+    if (jobs > 16 * kSms && longest < mean / 2) return longest;
+    const double fixed = 3.0;
+    int64_t best = longest;
+    double least = makespan(steps, d_.kv_heads, longest, fixed);
+    for (int k = 1; k <= 6; ++k) {
+      const int64_t most = std::max<int64_t>(4, (int64_t)std::ceil(mean / k));
+      if (most >= longest) continue;
+      const double t = makespan(steps, d_.kv_heads, most, fixed);
+      if (t < 0.97 * least) {
+        least = t;
+        best = most;
+      }
+    }
+    return best;
+  }
+
+  // Keys of a token item: small enough to give every SM its CTAs in one go
+  // where the keys are few, about three rounds of them where they are many.
+  int64_t token_range(const std::vector<PackedItem>& shared_tokens) const {
+    std::vector<int64_t> lens;
+    int64_t total = 0;
+    for (int s = 0; s < d_.num_seqs; ++s)
+      if (few_[s] && q_lens_[s] > 0 && kv_lens_[s] > 0) lens.push_back(kv_lens_[s]);
+    for (const PackedItem& t : shared_tokens) lens.push_back(t.pre_n);
+    for (int64_t l : lens) total += l;
+    const int64_t slots = 2 * kSms;  // CTAs resident at once
+    auto ctas = [&](int64_t range) {
+      int64_t n = 0;
+      for (int64_t l : lens) n += ceil_div(l, range);
+      return n * d_.kv_heads;
+    };
+    int64_t range = kChunk;
+    while (range < 2048 && ctas(range) > slots) range += kChunk;
+    return range;
+  }
+
+  tlsp_packed_desc d_;
+  const int32_t *q_lens_, *kv_lens_;
+  const int64_t* kv_starts_;
+  int group_, tile_tokens_;
+  std::vector<int64_t> q0_, kv0_;
+  std::vector<char> few_;
+  int64_t part_rows_ = 0;
+};
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// A [rows, heads, d] operand the kernels can read 16 bytes at a time.
+int validate_rows(const tlsp_rows* r, int64_t rows, int heads, int d, int size) {
+  if (rows == 0) return TLSP_OK;
+  if (!r || !r->ptr || !aligned16(r->ptr)) return TLSP_ERR_INVALID_ARG;
+  const int64_t unit = 16 / size;
+  if (rows > 1 && (r->row_stride < d || r->row_stride % unit)) return TLSP_ERR_INVALID_ARG;
+  if (heads > 1 && (r->head_stride < d || r->head_stride % unit)) return TLSP_ERR_INVALID_ARG;
+  return TLSP_OK;
+}
+
+// Strides of axes of length 1 are never used: set to something valid.
+tlsp_rows tidy(const tlsp_rows* r, int64_t rows, int heads, int d) {
+  tlsp_rows t{};
+  if (rows == 0) return t;
+  t = *r;
+  if (heads <= 1) t.head_stride = d;
+  if (rows <= 1) t.row_stride = (int64_t)heads * d;
+  return t;
+}
+
+int validate_packed(const tlsp_packed_plan* p) {
+  if (!p) return TLSP_ERR_INVALID_ARG;
+  TLSP_TRY(validate_desc(&p->desc));
+  if (p->tile_items < 0 || p->token_items < 0 || p->merge_items < 0 || p->q_rows < 0 ||
+      p->kv_rows < 0 || p->part_rows < 0 || p->q_rows > 0x7ffffeffLL || p->kv_rows > 0x7ffffeffLL)
+    return TLSP_ERR_INVALID_ARG;
+  return TLSP_OK;
+}
+
+int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* Q,
+              const tlsp_rows* Kp, const tlsp_rows* Vp, const tlsp_rows* K, const tlsp_rows* V,
+              const tlsp_rows* O, float* lse, float scale, void* ws, size_t ws_bytes,
+              void* stream) {
+  const tlsp_packed_desc& d = plan->desc;
+  const bool bf16 = d.dtype == TLSP_BF16;
+  const int size = bf16 ? 2 : 4;
+  if (!(std::fabs(scale) < INFINITY)) return TLSP_ERR_INVALID_ARG;
+  TLSP_TRY(validate_rows(Q, plan->q_rows, d.heads, d.head_dim, size));
+  TLSP_TRY(validate_rows(O, plan->q_rows, d.heads, d.head_dim, size));
+  TLSP_TRY(validate_rows(K, plan->kv_rows, d.kv_heads, d.head_dim, size));
+  TLSP_TRY(validate_rows(V, plan->kv_rows, d.kv_heads, d.head_dim, size));
+  TLSP_TRY(validate_rows(Kp, d.prefix_len, d.kv_heads, d.head_dim, size));
+  TLSP_TRY(validate_rows(Vp, d.prefix_len, d.kv_heads, d.head_dim, size));
+  if (!ws || !aligned16(ws) || (lse && (uintptr_t)lse % 4)) return TLSP_ERR_INVALID_ARG;
+  const WsLayout L = ws_layout(*plan);
+  if (ws_bytes < L.total) return TLSP_ERR_WORKSPACE;
+  if (plan->q_rows == 0) return TLSP_OK;
+  if (!items || !aligned16(items)) return TLSP_ERR_INVALID_ARG;
+  PackedArgs a{};
+  a.tiles = static_cast<const PackedItem*>(items);
+  a.tokens = a.tiles + plan->tile_items;
+  a.merges = reinterpret_cast<const MergeItem*>(a.tokens + plan->token_items);
+  a.n_tiles = plan->tile_items;
+  a.n_tokens = plan->token_items;
+  a.n_merges = plan->merge_items;
+  a.heads = d.heads;
+  a.kv_heads = d.kv_heads;
+  a.group = d.heads / d.kv_heads;
+  a.d = d.head_dim;
+  a.q_rows = plan->q_rows;
+  a.kv_rows = plan->kv_rows;
+  a.prefix_len = d.prefix_len;
+  a.part_rows = plan->part_rows;
+  a.Q = tidy(Q, plan->q_rows, d.heads, d.head_dim);
+  a.O = tidy(O, plan->q_rows, d.heads, d.head_dim);
+  a.K = tidy(K, plan->kv_rows, d.kv_heads, d.head_dim);
+  a.V = tidy(V, plan->kv_rows, d.kv_heads, d.head_dim);
+  a.Kp = tidy(Kp, d.prefix_len, d.kv_heads, d.head_dim);
+  a.Vp = tidy(Vp, d.prefix_len, d.kv_heads, d.head_dim);
+  a.lse = lse;
+  a.scale = scale != 0.f ? scale : 1.f / sqrtf((float)d.head_dim);
+  char* base = static_cast<char*>(ws);
+  a.status = reinterpret_cast<int*>(base);
+  a.part_lse = reinterpret_cast<float*>(base + L.lse);
+  a.part_o = reinterpret_cast<float*>(base + L.o);
+  cudaStream_t st = (cudaStream_t)stream;
+  TLSP_TRY(packed_simt(a, bf16, st));
+  if (a.n_merges > 0) TLSP_TRY(packed_merge(a, bf16, st));
+  return TLSP_OK;
+}
+
+}  // namespace
+}  // namespace tlsp
+
+using namespace tlsp;
+
+extern "C" {
+
+int tlsp_packed_make_plan(const tlsp_packed_desc* desc, const int32_t* q_lens,
+                          const int32_t* kv_lens, const int64_t* kv_starts, void* items,
+                          size_t items_bytes, tlsp_packed_plan* plan) {
+  TLSP_TRY(validate_desc(desc));
+  if (!q_lens || !kv_lens || !plan) return TLSP_ERR_INVALID_ARG;
+  try {
+    Planner p(*desc, q_lens, kv_lens, kv_starts);
+    TLSP_TRY(p.run());
+    tlsp_packed_plan out{};
+    out.desc = *desc;
+    out.tile_items = (int32_t)p.tiles.size();
+    out.token_items = (int32_t)p.tokens.size();
+    out.merge_items = (int32_t)p.merges.size();
+    out.q_rows = p.q_rows;
+    out.kv_rows = p.kv_rows;
+    out.part_rows = p.part_rows();
+    out.items_bytes =
+        sizeof(PackedItem) * (p.tiles.size() + p.tokens.size()) + sizeof(MergeItem) * p.merges.size();
+    out.ws_bytes = ws_layout(out).total;
+    *plan = out;
+    if (items_bytes < out.items_bytes || (out.items_bytes > 0 && !items)) return TLSP_ERR_WORKSPACE;
+    char* to = static_cast<char*>(items);
+    auto put = [&](const void* from, size_t bytes) {
+      if (bytes) std::memcpy(to, from, bytes);
+      to += bytes;
+    };
+    put(p.tiles.data(), sizeof(PackedItem) * p.tiles.size());
+    put(p.tokens.data(), sizeof(PackedItem) * p.tokens.size());
+    put(p.merges.data(), sizeof(MergeItem) * p.merges.size());
+  } catch (...) {  // out of host memory
+    return TLSP_ERR_UNSUPPORTED;
+  }
+  return TLSP_OK;
+}
+
+int tlsp_packed_attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* Q,
+                          const tlsp_rows* K, const tlsp_rows* V, const tlsp_rows* O, float* lse,
+                          float scale, void* ws, size_t ws_bytes, void* stream) {
+  TLSP_TRY(validate_packed(plan));
+  if (plan->desc.prefix_len != 0) return TLSP_ERR_INVALID_ARG;
+  return attention(plan, items, Q, nullptr, nullptr, K, V, O, lse, scale, ws, ws_bytes, stream);
+}
+
+int tlsp_prefix_attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* Q,
+                          const tlsp_rows* Kp, const tlsp_rows* Vp, const tlsp_rows* K,
+                          const tlsp_rows* V, const tlsp_rows* O, float* lse, float scale,
+                          void* ws, size_t ws_bytes, void* stream) {
+  TLSP_TRY(validate_packed(plan));
+  if (plan->desc.prefix_len < 1) return TLSP_ERR_INVALID_ARG;
+  return attention(plan, items, Q, Kp, Vp, K, V, O, lse, scale, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -26,17 +26,20 @@ class MCSparseAttention:
 
     Step s is an anchor step when `schedule` is given and schedule[s % len] is
     'A', else when s % anchor_every == 0 (so step 0 is always an anchor). A
-    change of shape, dtype or device forces an anchor step.
+    change of shape, dtype or device forces an anchor step. With `rotary`, Q and
+    K are turned by their positions first (out of place: the caller's stay).
     """
 
     def __init__(self, group_size: int, k: int, anchor_every: int = 2,
-                 schedule: Optional[Sequence[str]] = None):
+                 schedule: Optional[Sequence[str]] = None,
+                 rotary: Optional[tlsp.RotaryPlan] = None):
         if group_size < 1 or k < 1 or anchor_every < 1:
             raise ValueError("group_size, k and anchor_every must be >= 1")
         if schedule is not None and (not schedule or any(c not in "AR" for c in schedule)):
             raise ValueError("schedule must be a non-empty string of 'A' and 'R'")
         self.group_size, self.k, self.anchor_every = group_size, k, anchor_every
         self.schedule = None if schedule is None else "".join(schedule)
+        self.rotary = rotary
         self.step = 0
         self._key = None
         self.ws: Optional[tlsp.Workspace] = None
@@ -53,7 +56,26 @@ class MCSparseAttention:
         self.groups = self.indices = self.R = None
         self.step = 0
 
-    def __call__(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor) -> torch.Tensor:
+    def _turn(self, Q, K, positions, kv_positions):
+        if self.rotary is None:
+            if positions is not None or kv_positions is not None:
+                raise ValueError("positions need a rotary plan")
+            return Q, K
+        if positions is None:
+            raise ValueError("a rotary plan needs positions")
+        if kv_positions is None and Q.shape[2] == K.shape[2]:
+            return tlsp.rotary(Q, K, positions, self.rotary)
+        if kv_positions is None:
+            raise ValueError("keys of other tokens than the queries need kv_positions")
+        return (tlsp.rotary(Q, None, positions, self.rotary),
+                tlsp.rotary(K, None, kv_positions, self.rotary))
+
+    def __call__(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+                 positions: Optional[torch.Tensor] = None,
+                 kv_positions: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """One step. With a rotary plan: `positions` of the queries (tlsp.rotary's form) and
+        `kv_positions` of the keys where they are other tokens."""
+        Q, K = self._turn(Q, K, positions, kv_positions)
         key = (tuple(Q.shape), tuple(K.shape), Q.dtype, Q.device)
         anchor = self.is_anchor(self.step) or key != self._key
         if key != self._key:

@@ -35,6 +35,8 @@ EXPORTED = [
     "tlsp_reset_device_status", "tlsp_debug_bounded_wait", "tlsp_status_string",
     "tlsp_last_cuda_error", "tlsp_launch_count", "tlsp_group_raster",
     "tlsp_block_topk_from_scores", "tlsp_pooled_block_select",
+    "tlsp_rotary_make_plan", "tlsp_rotary", "tlsp_packed_make_plan", "tlsp_packed_attention",
+    "tlsp_prefix_attention",
 ]
 
 
@@ -47,6 +49,55 @@ class TlspError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("n_q", ctypes.c_int32),
                 ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("fast", ctypes.c_double),
+                ("slow", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class RotaryPlanData(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 128), ("turns", ctypes.c_uint64 * 128)]
+
+
+class RotaryTensor(ctypes.Structure):
+    _fields_ = ([("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)]
+                + [(n, ctypes.c_int64) for n in ("in_batch", "in_token", "in_head", "out_batch",
+                                                 "out_token", "out_head")]
+                + [("heads", ctypes.c_int32)])
+
+
+class RotaryCall(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("positions_64", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                ("position_axis", ctypes.c_int64), ("position_batch", ctypes.c_int64)]
+
+
+class PackedDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("causal", ctypes.c_int32),
+                ("prefix_len", ctypes.c_int32)]
+
+
+class PackedPlanData(ctypes.Structure):
+    _fields_ = [("desc", PackedDesc), ("tile_items", ctypes.c_int32),
+                ("token_items", ctypes.c_int32), ("merge_items", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("q_rows", ctypes.c_int64),
+                ("kv_rows", ctypes.c_int64), ("part_rows", ctypes.c_int64),
+                ("items_bytes", ctypes.c_uint64), ("ws_bytes", ctypes.c_uint64)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -86,6 +137,13 @@ def lib() -> ctypes.CDLL:
             "tlsp_block_topk_from_scores": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, vp, vp]),
             "tlsp_pooled_block_select": (ctypes.c_int,
                                          [dp, vp, vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]),
+            "tlsp_rotary_make_plan": (ctypes.c_int, [vp, vp]),
+            "tlsp_rotary": (ctypes.c_int, [vp, vp, vp, vp, i32, vp]),
+            "tlsp_packed_make_plan": (ctypes.c_int, [vp, vp, vp, vp, vp, sz, vp]),
+            "tlsp_packed_attention": (ctypes.c_int,
+                                      [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, sz, vp]),
+            "tlsp_prefix_attention": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                     ctypes.c_float, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -316,3 +374,299 @@ def pooled_block_select(Q: torch.Tensor, K: torch.Tensor, groups: torch.Tensor, 
                                           ws.nbytes, _stream()),
            "tlsp_pooled_block_select")
     return (idx, bs) if return_block_scores else idx
+
+
+# ----------------------------------------------------------------- rotary positions
+
+_ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROTARY_SCALINGS = {None: 0, "none": 0, "linear": 1, "base": 2, "ramp": 3}
+
+
+class RotaryPlan:
+    """Frequencies of a rotary embedding, made once and passed to every call (host memory only).
+
+    head_dim     channels of a head (a multiple of 8, at most 256)
+    rotary_dim   leading channels that are turned (default: all)
+    layout       "half": channel i pairs with i + rotary_dim / 2; "interleaved": 2i with 2i + 1
+    base         pair i of a section of s pairs turns by base^(-i / s) per position
+    scaling      None, "linear" (frequencies / factor), "base" (base * factor^(D / (D - 2))),
+                 "ramp" (pairs that turn fewer than `slow` times over original_len positions are
+                 divided by factor, those that turn more than `fast` times are kept, linear in
+                 between; amplitude 1 + 0.1 ln(factor) unless given)
+    sections     pairs of each position axis, e.g. (22, 21, 21) for (frame, row, column);
+                 default: one axis
+    """
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, base: float = 10000.0,
+                 layout: str = "half", scaling: Optional[str] = None, factor: float = 1.0,
+                 original_len: float = 0.0, fast: float = 32.0, slow: float = 1.0,
+                 amplitude: Optional[float] = None, sections=None):
+        if layout not in _ROTARY_LAYOUTS:
+            raise ValueError(f"layout must be one of {list(_ROTARY_LAYOUTS)}")
+        if scaling not in _ROTARY_SCALINGS:
+            raise ValueError(f"scaling must be one of {list(_ROTARY_SCALINGS)}")
+        if amplitude is not None and not amplitude > 0:
+            raise ValueError("amplitude must be positive")
+        r = head_dim if rotary_dim is None else rotary_dim
+        sec = [r // 2] if sections is None else [int(x) for x in sections]
+        if not 1 <= len(sec) <= 4:
+            raise ValueError("1 to 4 sections")
+        desc = RotaryDesc(head_dim, r, _ROTARY_LAYOUTS[layout], len(sec),
+                          (ctypes.c_int32 * 4)(*sec), _ROTARY_SCALINGS[scaling], base, factor,
+                          original_len, fast, slow, 0.0 if amplitude is None else amplitude)
+        self.data = RotaryPlanData()
+        _check(lib().tlsp_rotary_make_plan(ctypes.byref(desc), ctypes.byref(self.data)),
+               "tlsp_rotary_make_plan")
+        self.head_dim, self.rotary_dim, self.axes = head_dim, r, len(sec)
+
+
+def _on_device(device: torch.device):
+    """The stream to launch on: `device`'s current one (which need not be the current device)."""
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+class _Device:
+    """Makes `device` current for a launch if it is not."""
+
+    def __init__(self, device: torch.device):
+        self.guard = None
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _rotary_strides(x: torch.Tensor):
+    """(batch, token, head) strides of a [T, H, d] or [B, H, N, d] tensor."""
+    st = x.stride()
+    if st[-1] != 1:
+        raise ValueError("channels must be contiguous")
+    return (0, st[0], st[1]) if x.dim() == 3 else (st[0], st[2], st[1])
+
+
+def _rotary_tensor(x: torch.Tensor, out: torch.Tensor) -> RotaryTensor:
+    return RotaryTensor(x.data_ptr(), out.data_ptr(), *_rotary_strides(x), *_rotary_strides(out),
+                        x.shape[1])
+
+
+def _rotary(Q, K, positions, plan: RotaryPlan, out, backward: int):
+    many = K is not None
+    xs = (Q, K) if many else (Q,)
+    if Q.dim() not in (3, 4):
+        raise ValueError("tensors are [tokens, heads, head_dim] or [batch, heads, tokens, head_dim]")
+    batch, tokens = (1, Q.shape[0]) if Q.dim() == 3 else (Q.shape[0], Q.shape[2])
+    dev = Q.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the CUDA device")
+    code = _dtype_code(Q.dtype)
+    for x in xs:
+        if x.dim() != Q.dim() or x.dtype != Q.dtype or x.device != dev:
+            raise ValueError("queries and keys must have the same rank, type and device")
+        if x.shape[-1] != plan.head_dim or x.shape[1] < 1:
+            raise ValueError(f"expected heads of {plan.head_dim} channels, got {tuple(x.shape)}")
+        if (x.shape[0] if x.dim() == 3 else x.shape[2]) != tokens or (x.dim() == 4
+                                                                      and x.shape[0] != batch):
+            raise ValueError("queries and keys must have the same tokens")
+    if out is None:
+        outs = tuple(torch.empty(x.shape, dtype=x.dtype, device=dev) for x in xs)
+    else:
+        outs = tuple(out) if many else (out,)
+        if len(outs) != len(xs):
+            raise ValueError("out must be one tensor per input")
+        for x, o in zip(xs, outs):
+            if o.shape != x.shape or o.dtype != x.dtype or o.device != dev:
+                raise ValueError("out must match the input's shape, type and device")
+            if any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
+                raise ValueError("out must not be a broadcast tensor")
+    if positions.dtype not in (torch.int32, torch.int64) or positions.device != dev:
+        raise ValueError("positions must be int32 or int64 on the tensors' device")
+    shape, lead = tuple(positions.shape), (() if plan.axes == 1 else (plan.axes,))
+    if shape == lead + (tokens,):
+        p_batch = 0
+    elif Q.dim() == 4 and shape == lead + (batch, tokens):
+        p_batch = positions.stride(-2)
+    else:
+        raise ValueError(f"positions must be {lead + (tokens,)} (or with the batch before the "
+                         f"tokens), got {shape}")
+    if tokens > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions must be contiguous along the tokens")
+    call = RotaryCall(batch, tokens, code, positions.dtype == torch.int64, positions.data_ptr(),
+                      positions.stride(0) if lead else 0, p_batch)
+    ts = [_rotary_tensor(x, o) for x, o in zip(xs, outs)]
+    with _Device(dev):
+        _check(lib().tlsp_rotary(ctypes.byref(plan.data), ctypes.byref(call), ctypes.byref(ts[0]),
+                                 ctypes.byref(ts[1]) if many else None, backward,
+                                 _on_device(dev)), "tlsp_rotary")
+    return outs if many else outs[0]
+
+
+def rotary(Q: torch.Tensor, K: Optional[torch.Tensor], positions: torch.Tensor, plan: RotaryPlan,
+           out=None):
+    """Rotates queries and keys of the same tokens in one launch -> (Q', K') (Q' if K is None).
+
+    Q, K       [tokens, heads, head_dim] or [batch, heads, tokens, head_dim], any strides with
+               contiguous channels (slices of a fused projection, for instance)
+    positions  int32 or int64 [tokens] or [batch, tokens]; with several sections [axes, tokens]
+               or [axes, batch, tokens]
+    out        tensors to write (the inputs themselves: in place)
+    """
+    return _rotary(Q, K, positions, plan, out, 0)
+
+
+def rotary_backward(dQ: torch.Tensor, dK: Optional[torch.Tensor], positions: torch.Tensor,
+                    plan: RotaryPlan, out=None):
+    """Gradients of rotary()'s inputs from those of its outputs (the transposed map)."""
+    return _rotary(dQ, dK, positions, plan, out, 1)
+
+
+# ----------------------------------------------------------------- packed attention
+
+def _host_ints(values, ctype):
+    if isinstance(values, torch.Tensor):
+        if values.is_cuda:
+            raise ValueError("lengths are planned on the host: pass a list or a CPU tensor")
+        values = values.tolist()
+    values = list(values)
+    return (ctype * len(values))(*values), len(values)
+
+
+class PackedPlan:
+    """The work of a batch of packed sequences, laid out once and used by every layer.
+
+    q_lens, kv_lens  queries and keys of each sequence (host integers, each >= 0)
+    causal           query i of n sees keys j <= i + m - n of its sequence's m keys; else all m
+    prefix_len       keys of a prefix that every query of every sequence sees
+    kv_starts        first key row of each sequence (default: end to end), e.g. [0, cap, 2 * cap]
+                     for a cache of fixed capacity per sequence
+
+    The plan's table lives in device memory: keep the plan until the calls (and replays of
+    captured graphs) that use it have finished. Made outside of stream capture.
+    """
+
+    def __init__(self, q_lens, kv_lens, heads: int, kv_heads: int, head_dim: int,
+                 dtype: torch.dtype = torch.bfloat16, causal: bool = True, prefix_len: int = 0,
+                 kv_starts=None, device=None):
+        device = torch.device(device or "cuda")
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        q, n = _host_ints(q_lens, ctypes.c_int32)
+        kv, n_kv = _host_ints(kv_lens, ctypes.c_int32)
+        starts, n_st = (None, n) if kv_starts is None else _host_ints(kv_starts, ctypes.c_int64)
+        if n != n_kv or n != n_st:
+            raise ValueError("q_lens, kv_lens and kv_starts must have one entry per sequence")
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a plan is made outside of stream capture")
+        desc = PackedDesc(n, heads, kv_heads, head_dim, _dtype_code(dtype), bool(causal),
+                          prefix_len)
+        self.data = PackedPlanData()
+        table = bytearray(1 << 16)
+        while True:
+            buf = (ctypes.c_char * len(table)).from_buffer(table)
+            code = lib().tlsp_packed_make_plan(ctypes.byref(desc), q, kv, starts, buf, len(table),
+                                               ctypes.byref(self.data))
+            if code != TLSP_ERR_WORKSPACE:
+                break
+            table = bytearray(self.data.items_bytes)
+        _check(code, "tlsp_packed_make_plan")
+        self.heads, self.kv_heads, self.head_dim, self.dtype = heads, kv_heads, head_dim, dtype
+        self.prefix_len, self.device = prefix_len, device
+        self.q_rows, self.kv_rows = self.data.q_rows, self.data.kv_rows
+        used = max(self.data.items_bytes, 16)
+        # a blocking copy: the table is in place for every stream when this returns
+        self.items = torch.frombuffer(table, dtype=torch.uint8)[:used].to(device)
+        self._made_on = torch.cuda.current_stream(device).cuda_stream
+
+    def workspace(self) -> "Workspace":
+        """A workspace for calls with this plan (calls that overlap in time need one each)."""
+        return Workspace(None, nbytes=self.data.ws_bytes, device=self.device)
+
+
+def _packed_rows(t: Optional[torch.Tensor], what: str, rows: int, heads: int, plan: PackedPlan):
+    if t is None:
+        if rows:
+            raise ValueError(f"{what} is missing")
+        return None
+    if t.dim() != 3 or t.shape[0] < rows or t.shape[1] != heads or t.shape[2] != plan.head_dim:
+        raise ValueError(f"{what} must be [>= {rows}, {heads}, {plan.head_dim}], "
+                         f"got {tuple(t.shape)}")
+    if t.dtype != plan.dtype or t.device != plan.device:
+        raise ValueError(f"{what} must be {plan.dtype} on {plan.device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError(f"{what}: channels must be contiguous")
+    return ctypes.byref(Rows(t.data_ptr(), s0, s1))
+
+
+def _packed(Q, Kp, Vp, K, V, plan: PackedPlan, ws: Workspace, scale, out, lse):
+    what = "tlsp_prefix_attention" if plan.prefix_len else "tlsp_packed_attention"
+    q_rows, h, hk = plan.q_rows, plan.heads, plan.kv_heads
+    dev = plan.device
+    q = _packed_rows(Q, "Q", q_rows, h, plan)
+    k = _packed_rows(K, "K", plan.kv_rows, hk, plan)
+    v = _packed_rows(V, "V", plan.kv_rows, hk, plan)
+    if out is None:
+        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        if Q.shape[0] > q_rows:
+            out[q_rows:].zero_()
+    o = _packed_rows(out, "out", q_rows, h, plan)
+    lse_ptr = None
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.device != dev or lse.dim() != 2 or \
+                lse.shape[0] < q_rows or lse.shape[1] != h or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous fp32 [>= {q_rows}, {h}] on {dev}")
+        lse_ptr = lse.data_ptr()
+    if ws.buf.device != dev:
+        raise ValueError(f"the workspace must live on {dev}")
+    if scale is None:
+        scale = 0.0
+    elif scale == 0.0:
+        raise ValueError("scale must not be 0")
+    with _Device(dev):
+        stream = torch.cuda.current_stream(dev)
+        if stream.cuda_stream != plan._made_on and not torch.cuda.is_current_stream_capturing():
+            plan.items.record_stream(stream)  # its memory is not reused before this call is done
+            ws.buf.record_stream(stream)
+        st, items = ctypes.c_void_p(stream.cuda_stream), plan.items.data_ptr()
+        data = ctypes.byref(plan.data)
+        if plan.prefix_len:
+            kp = _packed_rows(Kp, "K_prefix", plan.prefix_len, hk, plan)
+            vp = _packed_rows(Vp, "V_prefix", plan.prefix_len, hk, plan)
+            code = lib().tlsp_prefix_attention(data, items, q, kp, vp, k, v, o, lse_ptr, scale,
+                                               ws.ptr, ws.nbytes, st)
+        else:
+            code = lib().tlsp_packed_attention(data, items, q, k, v, o, lse_ptr, scale, ws.ptr,
+                                               ws.nbytes, st)
+    _check(code, what)
+    return out
+
+
+def packed_attention(Q, K, V, plan: PackedPlan, ws: Workspace, scale: Optional[float] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """Attention over packed sequences (causal, grouped heads) -> O [tokens, heads, head_dim].
+
+    Q [tokens, heads, d], K, V [tokens, kv_heads, d]: sequences end to end (keys: at the plan's
+    kv_starts), any strides that are multiples of 16 bytes with contiguous channels. lse, if
+    given (fp32 [tokens, heads]), receives each row's log partition; rows that see no key get
+    O = 0 and lse = -inf. Rows of a given `out` (and lse) behind the last sequence are left as
+    they are; without `out` they are zero.
+    """
+    if plan.prefix_len:
+        raise ValueError("the plan has a prefix: call prefix_attention")
+    return _packed(Q, None, None, K, V, plan, ws, scale, out, lse)
+
+
+def prefix_attention(Q, K_prefix, V_prefix, K, V, plan: PackedPlan, ws: Workspace,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None):
+    """packed_attention in which every query also sees all keys of one shared prefix
+    (K_prefix, V_prefix [prefix_len, kv_heads, d]), which is read once for all short sequences.
+    K and V may be None when no sequence has keys of its own."""
+    if not plan.prefix_len:
+        raise ValueError("the plan has no prefix: call packed_attention")
+    return _packed(Q, K_prefix, V_prefix, K, V, plan, ws, scale, out, lse)
