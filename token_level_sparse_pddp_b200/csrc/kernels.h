@@ -58,6 +58,11 @@ int simt_sparse(const AttnArgs& a, const int32_t* groups, const int32_t* indices
 int make_tmap_bf16_rows(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
                         uint32_t box_cols, uint32_t box_rows);
 
+// bf16 map of `rank` axes (channels first), strides in elements of axes 1 ..
+// rank - 1, 128-byte swizzle.
+int make_tmap_bf16(CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box);
+
 // attn_tc.cu: tensor-core gathered sparse pass (bf16, d = 128)
 bool tc_attention_supported(const AttnArgs& a);
 int tc_sparse(const AttnArgs& a, const int32_t* groups, const int32_t* indices,

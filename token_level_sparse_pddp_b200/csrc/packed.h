@@ -33,8 +33,12 @@ constexpr int kTokenRows = 16;    // rows (tokens x heads of a group) of a token
 constexpr int kSimtTileRows = 64;  // rows of a tile item, fp32
 constexpr int kMergeTokens = 4;   // tokens of a merge item
 
-// Tokens of one tile: whole groups of `group` rows in `rows` rows.
-inline int tile_tokens(int rows, int group) { return rows / group; }
+constexpr int kTcRows = 128;       // rows of one of the two query tiles of a bf16 tile item
+
+// Most tokens of a tile item: whole groups of `group` rows per query tile.
+inline int tile_tokens(bool bf16, int group) {
+  return bf16 ? 2 * (kTcRows / group) : kSimtTileRows / group;
+}
 
 struct PackedArgs {
   const PackedItem* tiles;
@@ -51,10 +55,10 @@ struct PackedArgs {
   int* status;
 };
 
-// An item read from device memory lies within the call's tensors and `rows` rows
-// of a tile (else the caller's table is not the plan's: the item is skipped).
-__device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t, int rows) {
-  const bool pieces = t.nt >= 1 && t.nt * a.group <= rows && t.q0 >= 0 && t.kv0 >= 0 &&
+// An item read from device memory lies within the call's tensors and has at most
+// `tokens` tokens (else the caller's table is not the plan's: it is skipped).
+__device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t, int tokens) {
+  const bool pieces = t.nt >= 1 && t.nt <= tokens && t.q0 >= 0 && t.kv0 >= 0 &&
                       t.kv_n >= 0 && t.pre0 >= 0 && t.pre_n >= 0;
   return pieces && (int64_t)t.q0 + t.nt <= a.q_rows &&
          (t.kv_n == 0 || (int64_t)t.kv0 + t.kv_n <= a.kv_rows) &&
@@ -62,6 +66,8 @@ __device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t
          t.diag <= t.kv_n && (t.slot < 0 || (int64_t)t.slot + t.nt <= a.part_rows);
 }
 
+// packed_tile.cu: tile items on the tensor cores (bf16)
+int packed_tile(const PackedArgs& a, cudaStream_t st);
 int packed_simt(const PackedArgs& a, bool bf16, cudaStream_t st);
 int packed_merge(const PackedArgs& a, bool bf16, cudaStream_t st);
 

@@ -86,7 +86,7 @@ class Planner {
           const int64_t* kv_starts)
       : d_(d), q_lens_(q_lens), kv_lens_(kv_lens), kv_starts_(kv_starts) {
     group_ = d.heads / d.kv_heads;
-    tile_tokens_ = tile_tokens(kSimtTileRows, group_);
+    tile_tokens_ = tile_tokens(d.dtype == TLSP_BF16, group_);
   }
 
   int run() {
@@ -404,6 +404,7 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   a.part_lse = reinterpret_cast<float*>(base + L.lse);
   a.part_o = reinterpret_cast<float*>(base + L.o);
   cudaStream_t st = (cudaStream_t)stream;
+  if (bf16 && a.n_tiles > 0) TLSP_TRY(packed_tile(a, st));
   TLSP_TRY(packed_simt(a, bf16, st));
   if (a.n_merges > 0) TLSP_TRY(packed_merge(a, bf16, st));
   return TLSP_OK;

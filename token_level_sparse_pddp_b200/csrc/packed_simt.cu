@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kThreads)
   float* sP = sV + kBN * LD;
   const PackedItem it = items[blockIdx.x / p.kv_heads];
   const int hk = blockIdx.x % p.kv_heads;
-  if (!item_ok(p, it, BM)) {
+  if (!item_ok(p, it, BM / p.group)) {
     if (threadIdx.x == 0) record_status(p.status, TLSP_ERR_DEVICE_ASSERT);
     return;
   }
@@ -213,7 +213,7 @@ int launch(const PackedArgs& a, const PackedItem* items, int n, cudaStream_t st)
 
 template <class T, int D>
 int run(const PackedArgs& a, cudaStream_t st) {
-  TLSP_TRY((launch<T, D, kSimtTileRows>(a, a.tiles, a.n_tiles, st)));
+  if (sizeof(T) == 4) TLSP_TRY((launch<T, D, kSimtTileRows>(a, a.tiles, a.n_tiles, st)));
   return launch<T, D, kTokenRows>(a, a.tokens, a.n_tokens, st);
 }
 

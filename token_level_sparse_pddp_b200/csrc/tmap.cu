@@ -36,4 +36,18 @@ int make_tmap_bf16_rows(CUtensorMap* map, const void* ptr, uint64_t rows, uint64
   return r == CUDA_SUCCESS ? TLSP_OK : TLSP_ERR_CUDA;
 }
 
+int make_tmap_bf16(CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box) {
+  auto fn = encode_fn();
+  if (!fn) return TLSP_ERR_CUDA;
+  cuuint64_t bytes[4];
+  for (int i = 0; i + 1 < rank; ++i) bytes[i] = strides[i] * 2;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr),
+                  reinterpret_cast<const cuuint64_t*>(dims), bytes, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TLSP_OK : TLSP_ERR_INVALID_ARG;  // strides the maps cannot hold
+}
+
 }  // namespace tlsp
