@@ -68,7 +68,11 @@ __device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t
 
 // packed_tile.cu: tile items on the tensor cores (bf16)
 int packed_tile(const PackedArgs& a, cudaStream_t st);
-int packed_simt(const PackedArgs& a, bool bf16, cudaStream_t st);
+// packed_token.cu: token items (bf16)
+int packed_token(const PackedArgs& a, cudaStream_t st);
+// packed_simt.cu: both kinds of items (fp32)
+int packed_simt(const PackedArgs& a, cudaStream_t st);
+// packed_merge.cu: merge items
 int packed_merge(const PackedArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace tlsp

@@ -404,8 +404,12 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   a.part_lse = reinterpret_cast<float*>(base + L.lse);
   a.part_o = reinterpret_cast<float*>(base + L.o);
   cudaStream_t st = (cudaStream_t)stream;
-  if (bf16 && a.n_tiles > 0) TLSP_TRY(packed_tile(a, st));
-  TLSP_TRY(packed_simt(a, bf16, st));
+  if (bf16) {
+    if (a.n_tiles > 0) TLSP_TRY(packed_tile(a, st));
+    if (a.n_tokens > 0) TLSP_TRY(packed_token(a, st));
+  } else {
+    TLSP_TRY(packed_simt(a, st));
+  }
   if (a.n_merges > 0) TLSP_TRY(packed_merge(a, bf16, st));
   return TLSP_OK;
 }

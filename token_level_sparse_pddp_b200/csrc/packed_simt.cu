@@ -1,4 +1,5 @@
-// Packed attention on the CUDA cores.
+// Packed attention of fp32 tensors, on the CUDA cores (tensor cores round the
+// operands to 19 bits or fewer).
 //
 // One CTA per (item, key/value head): its rows (tokens x query heads of the
 // group) against blocks of 64 keys, with the running maximum and sum of the
@@ -20,7 +21,7 @@ constexpr int smem_floats() {
   return BM * (D + 4) + 2 * kBN * (D + 4) + BM * (kBN + 4);
 }
 
-template <class T, int D, int BM>
+template <int D, int BM>
 __global__ void __launch_bounds__(kThreads)
     packed_simt_kernel(const __grid_constant__ PackedArgs p, const PackedItem* items) {
   constexpr int RM = BM / 16, DV = D / 16, LD = D + 4, LP = kBN + 4;
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(kThreads)
   const float scale = p.scale * 1.4426950408889634f;
 
   // Q rows r = token * group + head of the group
-  const T* Q = static_cast<const T*>(p.Q.ptr);
+  const float* Q = static_cast<const float*>(p.Q.ptr);
   for (int e = threadIdx.x; e < BM * (D / 8); e += kThreads) {
     const int r = e / (D / 8), c = e % (D / 8) * 8;
     float x[8] = {};
@@ -71,8 +72,8 @@ __global__ void __launch_bounds__(kThreads)
     const tlsp_rows& KR = pre ? p.Kp : p.K;
     const tlsp_rows& VR = pre ? p.Vp : p.V;
     const int64_t row0 = (int64_t)(pre ? it.pre0 : it.kv0) + k0;
-    const T* K = static_cast<const T*>(KR.ptr) + row0 * KR.row_stride + hk * KR.head_stride;
-    const T* V = static_cast<const T*>(VR.ptr) + row0 * VR.row_stride + hk * VR.head_stride;
+    const float* K = static_cast<const float*>(KR.ptr) + row0 * KR.row_stride + hk * KR.head_stride;
+    const float* V = static_cast<const float*>(VR.ptr) + row0 * VR.row_stride + hk * VR.head_stride;
     __syncthreads();
     for (int e = threadIdx.x; e < kBN * (D / 8); e += kThreads) {
       const int r = e / (D / 8), c = e % (D / 8) * 8;
@@ -186,10 +187,10 @@ __global__ void __launch_bounds__(kThreads)
     const float inv = none ? 0.f : 1.f / l[a];
     const float lse = none ? -INFINITY : (m[a] + log2f(l[a])) * 0.6931471805599453f;
     if (it.slot < 0) {
-      T* o = static_cast<T*>(p.O.ptr) + (it.q0 + i) * p.O.row_stride + h * p.O.head_stride;
+      float* o = static_cast<float*>(p.O.ptr) + (it.q0 + i) * p.O.row_stride + h * p.O.head_stride;
 #pragma unroll
       for (int c = 0; c < DV; ++c)
-        o[tx * 4 + (c / 4) * 64 + c % 4] = from_f32<T>(none ? 0.f : acc[a][c] * inv);
+        o[tx * 4 + (c / 4) * 64 + c % 4] = none ? 0.f : acc[a][c] * inv;
       if (p.lse && tx == 0) p.lse[(int64_t)(it.q0 + i) * p.heads + h] = lse;
     } else {
       const int64_t row = (int64_t)(it.slot + i) * p.heads + h;
@@ -201,109 +202,26 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <class T, int D, int BM>
+template <int D, int BM>
 int launch(const PackedArgs& a, const PackedItem* items, int n, cudaStream_t st) {
   if (n == 0) return TLSP_OK;
-  auto kernel = packed_simt_kernel<T, D, BM>;
+  auto kernel = packed_simt_kernel<D, BM>;
   constexpr int bytes = smem_floats<D, BM>() * (int)sizeof(float);
   TLSP_TRY(ensure_smem_limit((const void*)kernel, bytes));
   kernel<<<(unsigned)((int64_t)n * a.kv_heads), kThreads, bytes, st>>>(a, items);
   return check_launch();
 }
 
-template <class T, int D>
+template <int D>
 int run(const PackedArgs& a, cudaStream_t st) {
-  if (sizeof(T) == 4) TLSP_TRY((launch<T, D, kSimtTileRows>(a, a.tiles, a.n_tiles, st)));
-  return launch<T, D, kTokenRows>(a, a.tokens, a.n_tokens, st);
-}
-
-// Partial results of a row over its key ranges: O = sum_p e^(lse_p - lse) O_p
-// with lse = log sum_p e^(lse_p). One warp per row.
-template <class T, int D>
-__global__ void __launch_bounds__(256)
-    packed_merge_kernel(const __grid_constant__ PackedArgs p) {
-  const MergeItem it = p.merges[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + warp;
-  if (row >= it.nt * p.heads) return;
-  const int i = row / p.heads, h = row % p.heads;
-  const int parts = it.a_parts + it.b_parts;
-  const bool ok = it.q0 >= 0 && it.nt >= 1 && (int64_t)it.q0 + it.nt <= p.q_rows &&
-                  it.a_parts >= 0 && it.b_parts >= 0 && it.a_slot >= 0 && it.b_slot >= 0 &&
-                  it.a_stride >= 0 && it.b_stride >= 0 &&
-                  (it.a_parts == 0 || it.a_slot + (int64_t)(it.a_parts - 1) * it.a_stride + it.nt <=
-                                          p.part_rows) &&
-                  (it.b_parts == 0 || it.b_slot + (int64_t)(it.b_parts - 1) * it.b_stride + it.nt <=
-                                          p.part_rows);
-  if (!ok) {
-    if (lane == 0) record_status(p.status, TLSP_ERR_DEVICE_ASSERT);
-    return;
-  }
-  auto part_row = [&](int q) {
-    const int64_t slot = q < it.a_parts
-                             ? it.a_slot + (int64_t)q * it.a_stride
-                             : it.b_slot + (int64_t)(q - it.a_parts) * it.b_stride;
-    return (slot + i) * p.heads + h;
-  };
-  float mx = -INFINITY;
-  for (int q = lane; q < parts; q += 32) mx = fmaxf(mx, p.part_lse[part_row(q)]);
-  mx = warp_max(mx);
-  const float m_use = mx == -INFINITY ? 0.f : mx;
-  constexpr int E = D / 32;
-  float acc[E] = {};
-  float sum = 0.f;
-  for (int q0 = 0; q0 < parts; q0 += 32) {
-    // a part that saw no key (lse -inf) has weight 0 and O = 0
-    const float w_lane = q0 + lane < parts ? expf(p.part_lse[part_row(q0 + lane)] - m_use) : 0.f;
-    const int n = min(32, parts - q0);
-#pragma unroll 4
-    for (int q = 0; q < n; ++q) {
-      const float w = __shfl_sync(0xffffffffu, w_lane, q);
-      const float* o = p.part_o + part_row(q0 + q) * D + lane * E;
-      sum += w;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-      }
-    }
-  }
-  const bool none = sum == 0.f;
-  const float inv = none ? 0.f : 1.f / sum;
-  T* o = static_cast<T*>(p.O.ptr) + (it.q0 + i) * p.O.row_stride + h * p.O.head_stride + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = from_f32<T>(acc[e] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)(it.q0 + i) * p.heads + h] = none ? -INFINITY : m_use + logf(sum);
-}
-
-template <class T>
-int merge(const PackedArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)a.n_merges, (unsigned)ceil_div((int64_t)kMergeTokens * a.heads, 8));
-  if (grid.y > 65535) return TLSP_ERR_UNSUPPORTED;
-  if (a.d == 128)
-    packed_merge_kernel<T, 128><<<grid, 256, 0, st>>>(a);
-  else
-    packed_merge_kernel<T, 64><<<grid, 256, 0, st>>>(a);
-  return check_launch();
+  TLSP_TRY((launch<D, kSimtTileRows>(a, a.tiles, a.n_tiles, st)));
+  return launch<D, kTokenRows>(a, a.tokens, a.n_tokens, st);
 }
 
 }  // namespace
 
-int packed_simt(const PackedArgs& a, bool bf16, cudaStream_t st) {
-  if (bf16)
-    return a.d == 128 ? run<__nv_bfloat16, 128>(a, st) : run<__nv_bfloat16, 64>(a, st);
-  return a.d == 128 ? run<float, 128>(a, st) : run<float, 64>(a, st);
-}
-
-int packed_merge(const PackedArgs& a, bool bf16, cudaStream_t st) {
-  return bf16 ? merge<__nv_bfloat16>(a, st) : merge<float>(a, st);
+int packed_simt(const PackedArgs& a, cudaStream_t st) {
+  return a.d == 128 ? run<128>(a, st) : run<64>(a, st);
 }
 
 }  // namespace tlsp
