@@ -19,6 +19,24 @@ def T():
     return tlsp
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class RotaryTensor(ctypes.Structure):
+    _fields_ = ([("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)]
+                + [(n, ctypes.c_int64) for n in ("in_batch", "in_token", "in_head", "out_batch",
+                                                 "out_token", "out_head")]
+                + [("heads", ctypes.c_int32)])
+
+
+class RotaryCall(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("positions_64", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                ("position_axis", ctypes.c_int64), ("position_batch", ctypes.c_int64)]
+
+
 def make(T, q, kv, heads=4, kv_heads=2, d=128, dtype=1, causal=1, prefix=0, starts=None):
     desc = T.PackedDesc(len(q), heads, kv_heads, d, dtype, causal, prefix)
     data = T.PackedPlanData()
@@ -164,7 +182,7 @@ def test_attention_refusals(T):
     p = ctypes.c_void_p(0x10000)      # never dereferenced
 
     def rows(heads, ptr=0x10000, rs=None, hs=128):
-        return ctypes.byref(T.Rows(ptr, heads * 128 if rs is None else rs, hs))
+        return ctypes.byref(Rows(ptr, heads * 128 if rs is None else rs, hs))
     ok = dict(plan=ctypes.byref(data), items=p, Q=rows(4), K=rows(2), V=rows(2), O=rows(4), lse=None,
               scale=0.0, ws=p, n=1 << 40)
 
@@ -225,6 +243,15 @@ def test_rotary_frequencies(T, kw):
     assert abs(plan.data.amplitude - amp) <= 2 ** -23 * amp
 
 
+def test_struct_layouts(T):
+    """The bytes the binding packs are the structs' layouts."""
+    assert T._ROTARY_TENSOR.size == ctypes.sizeof(RotaryTensor)
+    assert T._ROTARY_CALL.size == ctypes.sizeof(RotaryCall) and T._ROWS.size == ctypes.sizeof(Rows)
+    a = T._ROTARY_TENSOR.pack(*range(1, 10))
+    assert a == bytes(RotaryTensor(*range(1, 10)))
+    assert T._ROTARY_CALL.pack(*range(1, 8)) == bytes(RotaryCall(*range(1, 8)))
+
+
 def test_rotary_refusals(T):
     for kw in (dict(head_dim=100), dict(head_dim=264), dict(head_dim=0), dict(rotary_dim=63),
                dict(rotary_dim=130), dict(rotary_dim=0), dict(base=0.0), dict(base=math.inf),
@@ -243,20 +270,20 @@ def test_rotary_refusals(T):
     plan = T.RotaryPlan(128).data
 
     def call(c=None, q=None, k=None, backward=0, plan=plan):
-        c = T.RotaryCall(1, 4, 1, 0, 0x10000, 0, 0) if c is None else c
-        q = T.RotaryTensor(0x10000, 0x20000, 0, 128, 512, 0, 128, 512, 2) if q is None else q
+        c = RotaryCall(1, 4, 1, 0, 0x10000, 0, 0) if c is None else c
+        q = RotaryTensor(0x10000, 0x20000, 0, 128, 512, 0, 128, 512, 2) if q is None else q
         return L.tlsp_rotary(ctypes.byref(plan), ctypes.byref(c), ctypes.byref(q),
                              None if k is None else ctypes.byref(k), backward, None)
-    assert call(c=T.RotaryCall(1, 0, 1, 0, 0x10000, 0, 0)) == T.TLSP_OK      # no tokens
-    for c in (T.RotaryCall(-1, 4, 1, 0, 0x10000, 0, 0), T.RotaryCall(1, -4, 1, 0, 0x10000, 0, 0),
-              T.RotaryCall(1, 4, 7, 0, 0x10000, 0, 0), T.RotaryCall(1, 4, 1, 0, 0, 0, 0),
-              T.RotaryCall(1, 4, 1, 1, 0x10004, 0, 0)):
+    assert call(c=RotaryCall(1, 0, 1, 0, 0x10000, 0, 0)) == T.TLSP_OK      # no tokens
+    for c in (RotaryCall(-1, 4, 1, 0, 0x10000, 0, 0), RotaryCall(1, -4, 1, 0, 0x10000, 0, 0),
+              RotaryCall(1, 4, 7, 0, 0x10000, 0, 0), RotaryCall(1, 4, 1, 0, 0, 0, 0),
+              RotaryCall(1, 4, 1, 1, 0x10004, 0, 0)):
         assert call(c=c) == E
-    for q in (T.RotaryTensor(0, 0x20000, 0, 128, 512, 0, 128, 512, 2),
-              T.RotaryTensor(0x10000, 0, 0, 128, 512, 0, 128, 512, 2),
-              T.RotaryTensor(0x10001, 0x20000, 0, 128, 512, 0, 128, 512, 2),
-              T.RotaryTensor(0x10000, 0x10000, 0, 128, 512, 0, 256, 512, 2),   # in place, other strides
-              T.RotaryTensor(0x10000, 0x20000, 0, 128, 512, 0, 128, 512, 0)):
+    for q in (RotaryTensor(0, 0x20000, 0, 128, 512, 0, 128, 512, 2),
+              RotaryTensor(0x10000, 0, 0, 128, 512, 0, 128, 512, 2),
+              RotaryTensor(0x10001, 0x20000, 0, 128, 512, 0, 128, 512, 2),
+              RotaryTensor(0x10000, 0x10000, 0, 128, 512, 0, 256, 512, 2),   # in place, other strides
+              RotaryTensor(0x10000, 0x20000, 0, 128, 512, 0, 128, 512, 0)):
         assert call(q=q) == E and call(k=q) == E
     assert call(backward=2) == E
     broken = T.RotaryPlan(128).data

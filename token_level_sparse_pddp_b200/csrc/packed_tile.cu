@@ -6,25 +6,34 @@
 // K and V tiles; an item has one or two query tiles of up to 128 rows, and both
 // take each chunk of 128 keys (prefix keys, then own keys) from the same shared
 // memory: each key tile is read once for 256 rows.
-// Warp roles (384 threads, one CTA per SM):
-//   warps 0-3, 4-7  softmax and epilogue of query tile 0, 1: thread t owns row t
-//                   = TMEM lane t;
-//   warp 8          lane 0 loads Q, K and V with TMA box loads (128-byte swizzle;
+// Warp roles (640 threads, one CTA per SM):
+//   warps 0-7, 8-15 softmax and epilogue of query tile 0, 1: two threads share a row
+//                   (= TMEM lane), one for keys 0-63 of each chunk, one for 64-127:
+//                   four warps on each sub-partition, which keeps its special-
+//                   function unit busy through each other's waits (two: 70%);
+//   warp 16         lane 0 loads Q, K and V with TMA box loads (128-byte swizzle;
 //                   three K and two V slots);
-//   warp 9          allocates TMEM; lane 0 issues the tcgen05.mma instructions;
-//   warp 10         guards V: in the last chunk of a key range the rows behind it
+//   warps 17, 18    issue the tcgen05.mma instructions, Q K^T and P V (17 allocates
+//                   TMEM). Each stays converged and elects one lane to issue, so
+//                   that descriptors live in uniform registers (issuing from a
+//                   divergent branch took 57 cycles per MMA, nearly the 64 that the
+//                   MMA takes), and one's waits do not hold up the other;
+//   warp 19         guards V: in the last chunk of a key range the rows behind it
 //                   are zeroed, and in chunks that only part of the rows see,
 //                   values that are not finite are taken out (a masked key has
 //                   weight 0, and 0 x inf is NaN) and noted; the epilogue adds
 //                   them to the rows that do see them.
-// Per chunk and tile: S = Q K^T (fp32 in TMEM), P = 2^(S scale - m) in one pass,
-// written over S as bf16, O += P V with A = P from TMEM. The two tiles take turns:
-// while one's softmax runs, the tensor cores work on the other's P V and next
-// Q K^T. TMEM columns: S0, S1 [0, 256), O0, O1 [256, 256 + 2 d).
-// The reference m of a row is the maximum of the first 32 scores it sees; it is
-// raised (and O rescaled in TMEM) only when a chunk's sum of P exceeds 2^8, which
-// any score more than 8 (in log2) above m causes. P is rounded to bf16 (2^-8
-// relative, the type the tensor cores take); sums and O stay fp32.
+// Per chunk and tile: S = Q K^T (fp32 in TMEM), P = 2^(S scale - m) as bf16 in
+// TMEM, O += P V with A = P from TMEM. TMEM columns: one S buffer [0, 128) that
+// both tiles share, P0, P1 [128, 256), O0, O1 [256, 256 + 2 d). A row's thread
+// takes its whole row of S into registers at once, so the buffer is free for the
+// other tile's Q K^T after some 0.2 K cycles of the softmax, and
+// each tile's next scores are there when its softmax has finished. (With S of
+// each tile in a buffer of its own and P written over it, a chunk of a tile went
+// through softmax, P V and Q K^T one after the other: 3.5 K cycles.)
+// The reference m of a row is raised (and O rescaled in TMEM) only when a chunk's
+// maximum passes it by more than 8 (log2). P is rounded to bf16 (2^-8 relative,
+// the type the tensor cores take); sums and O stay fp32.
 // Every wait is bounded (1 s); on expiry the kernel records TLSP_ERR_TIMEOUT,
 // drains its own copies and MMAs, frees TMEM and returns.
 #include <algorithm>
@@ -36,12 +45,12 @@ namespace tlsp {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kGuardWarp = 10;
+constexpr int kThreads = 640;
+constexpr int kLoadWarp = 16, kQkWarp = 17, kPvWarp = 18, kGuardWarp = 19;
 constexpr int kKSlots = 3, kVSlots = 2;
 constexpr uint32_t kHalfBytes = kTile * 128;  // 128 rows of 64 channels
 constexpr uint32_t kTmCols = 512;
-constexpr uint32_t kTmO = 256;
+constexpr uint32_t kTmP = 128, kTmO = 256;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -51,7 +60,10 @@ struct Smem {
   static constexpr uint32_t q = 0;
   static constexpr uint32_t k = 2 * tile;
   static constexpr uint32_t v = (2 + kKSlots) * tile;
-  static constexpr uint32_t bar = (2 + kKSlots + kVSlots) * tile;
+  // 128 rows x 256 bytes of output per query tile: over its Q where that is as large
+  static constexpr uint32_t stage_bytes = kTile * 256;
+  static constexpr uint32_t stage = D == 128 ? q : (2 + kKSlots + kVSlots) * tile;
+  static constexpr uint32_t bar = (2 + kKSlots + kVSlots) * tile + (D == 128 ? 0 : 2 * stage_bytes);
   static constexpr uint32_t bytes = bar + 512 + 1024;  // + slack to align the base
 };
 
@@ -59,7 +71,7 @@ struct Bars {
   uint64_t q_full;
   uint64_t k_full[kKSlots], k_empty[kKSlots];
   uint64_t v_full[kVSlots], v_ready[kVSlots], v_empty[kVSlots];
-  uint64_t s_full[2], p_full[2], o_final[2], drain;
+  uint64_t s_full[2], s_free, p_full[2], pv_done[2], drain[2];
   uint32_t tmem_base;
   int abort;
   uint32_t odd[8];  // own keys diag + 1 + bit whose V holds a value that is not finite
@@ -83,10 +95,30 @@ __device__ __forceinline__ void fail(Bars& b, int* status) {
   record_status(status, TLSP_ERR_TIMEOUT);
 }
 
-// Both bf16 halves of a word: bits of those that are not finite.
+// Bit 15 and bit 31 tell which bf16 halves of a word are not finite (exponent all
+// ones: adding one to it carries into the sign's place).
+__device__ __forceinline__ uint32_t exp_carry(uint32_t w) {
+  return (w & 0x7f807f80u) + 0x00800080u;
+}
+// All bits of those halves.
 __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
   return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
          ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+// Barrier of `threads` threads; true if `vote` was, in any of them.
+__device__ __forceinline__ bool bar_or(int id, int threads, bool vote) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)vote), "r"(id), "r"(threads)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 template <int D>
@@ -131,15 +163,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&bars.s_full[s], 1);
-      ptx::mbar_init(&bars.p_full[s], 128);
-      ptx::mbar_init(&bars.o_final[s], 1);
+      ptx::mbar_init(&bars.p_full[s], 8);  // warps
+      ptx::mbar_init(&bars.pv_done[s], 1);
     }
-    ptx::mbar_init(&bars.drain, 1);
+    ptx::mbar_init(&bars.s_free, 8);
+    ptx::mbar_init(&bars.drain[0], 1);
+    ptx::mbar_init(&bars.drain[1], 1);
     bars.abort = 0;
     for (int i = 0; i < 8; ++i) bars.odd[i] = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     ptx::tmem_alloc(&bars.tmem_base, kTmCols);
     ptx::tmem_relinquish();
   }
@@ -195,68 +229,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n_chunks > 0) {
+  } else if (warp == kQkWarp || warp == kPvWarp) {
+    // ------------------------------------------------------------ MMA issuers
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+      ok = ok && ptx::mbar_spin(bar, parity & 1, abort_flag, kWaitNs);
+    };
+    if (warp == kQkWarp && n_chunks > 0) {
       constexpr uint32_t id_qk = ptx::idesc_bf16(kTile, kTile, false);
-      constexpr uint32_t id_pv = ptx::idesc_bf16(kTile, D, true);
-      bool ok = ptx::mbar_wait(&bars.q_full, 0, abort_flag, kWaitNs);
-      auto qk = [&](int s, int j) {  // S_s = Q_s K_j^T
-        const uint32_t qb = base + S::q + s * S::tile, kb = base + S::k + (j % kKSlots) * S::tile;
+      wait(&bars.q_full, 0);
+      int scores = 0;  // Q K^T issued so far
+      for (int j = 0; j < n_chunks; ++j) {
+        wait(&bars.k_full[j % kKSlots], j / kKSlots);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32u;
-          ptx::mma_ss(tmem + s * kTile, ptx::sw128_desc(qb + off, 16, 1024),
-                      ptx::sw128_desc(kb + off, 16, 1024), id_qk, kk > 0 ? 1u : 0u);
-        }
-        ptx::tc_commit(&bars.s_full[s]);
-      };
-      auto pv = [&](int s, int j) {  // O_s += P_s V_j
-        const uint32_t vb = base + S::v + (j % kVSlots) * S::tile;
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          ptx::mma_ts(tmem + kTmO + s * D, tmem + s * kTile + kk * 8,
-                      ptx::sw128_desc(vb + kk * 2048, kHalfBytes, 1024), id_pv,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-      };
-      auto wait_k = [&](int j) {
-        ok = ok && ptx::mbar_wait(&bars.k_full[j % kKSlots], (j / kKSlots) & 1, abort_flag, kWaitNs);
-        ptx::tc_fence_after();
-      };
-      wait_k(0);
-      if (ok) {
-        if (n0 > 0) qk(0, 0);
-        if (n1 > 0) qk(1, 0);
-        ptx::tc_commit(&bars.k_empty[0]);
-      }
-      for (int j = 0; j < n_chunks && ok; ++j) {
-        // the last tile that takes chunk j (and j + 1) releases its slots
-        ok = ptx::mbar_wait(&bars.v_ready[j % kVSlots], (j / kVSlots) & 1, abort_flag, kWaitNs);
-        if (j + 1 < n_chunks) wait_k(j + 1);
-        const bool last1 = j < n1;
-#pragma unroll 1
-        for (int s = 0; s < 2 && ok; ++s) {
-          const int n = s == 0 ? n0 : n1;
-          if (j >= n) continue;
-          ok = ptx::mbar_wait(&bars.p_full[s], j & 1, abort_flag, kWaitNs);
-          if (!ok) break;
-          ptx::fence_proxy_async_smem();
+        for (int s = 0; s < 2; ++s) {  // S = Q_s K_j^T, once the S before has been read
+          if (j >= (s == 0 ? n0 : n1)) continue;
+          if (scores > 0) wait(&bars.s_free, scores - 1);
+          ++scores;
+          if (!__all_sync(0xffffffffu, ok)) break;
           ptx::tc_fence_after();
-          pv(s, j);
-          if (s == 1 || !last1) ptx::tc_commit(&bars.v_empty[j % kVSlots]);
-          if (j == n - 1) ptx::tc_commit(&bars.o_final[s]);
-          if (j + 1 < n) {
-            qk(s, j + 1);
-            if (s == 1 || j + 1 >= n1) ptx::tc_commit(&bars.k_empty[(j + 1) % kKSlots]);
+          if (ptx::elect_one()) {
+            const uint64_t qd = ptx::sw128_desc(base + S::q + s * S::tile, 16, 1024);
+            const uint64_t kd = ptx::sw128_desc(base + S::k + (j % kKSlots) * S::tile, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32u;
+              ptx::mma_ss(tmem, qd + (off >> 4), kd + (off >> 4), id_qk, kk > 0 ? 1u : 0u);
+            }
+            ptx::tc_commit(&bars.s_full[s]);
+            if (s == 1 || j >= n1) ptx::tc_commit(&bars.k_empty[j % kKSlots]);  // its last use
           }
+          __syncwarp();
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
       }
+    }
+    if (warp == kPvWarp) {
+      constexpr uint32_t id_pv = ptx::idesc_bf16(kTile, D, true);
+      for (int j = 0; j < n_chunks; ++j) {
+        wait(&bars.v_ready[j % kVSlots], j / kVSlots);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {  // O_s += P_s V_j
+          if (j >= (s == 0 ? n0 : n1)) continue;
+          wait(&bars.p_full[s], j);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t vd =
+                ptx::sw128_desc(base + S::v + (j % kVSlots) * S::tile, kHalfBytes, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              ptx::mma_ts(tmem + kTmO + s * D, tmem + kTmP + s * 64 + kk * 8,
+                          vd + kk * (2048 >> 4), id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            ptx::tc_commit(&bars.pv_done[s]);
+            if (s == 1 || j >= n1) ptx::tc_commit(&bars.v_empty[j % kVSlots]);
+          }
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+    }
+    // all issued MMAs must land before TMEM is released, even after an abort
+    uint64_t* drain = &bars.drain[warp - kQkWarp];
+    __syncwarp();
+    if (ptx::elect_one()) {
       if (!ok) fail(bars, p.a.status);
-      // all issued MMAs must land before TMEM is released
-      ptx::tc_commit(&bars.drain);
-      ptx::mbar_wait(&bars.drain, 0, nullptr, kWaitNs);  // even after an abort
+      ptx::tc_commit(drain);
     }
     __syncwarp();
+    ptx::mbar_wait(drain, 0, nullptr, kWaitNs);
   } else if (warp == kGuardWarp) {
     // ------------------------------------------------------------ V guard
     for (int j = 0; j < n_chunks; ++j) {
@@ -276,200 +319,209 @@ __global__ void __launch_bounds__(kThreads, 1)
         every = min(some, max(0, it.diag + 1 - c));
       }
       if (every < kTile) {
-        uint8_t* v = smem + S::v + vs * S::tile;
+        const uint32_t v = base + S::v + vs * S::tile;
         for (int h = 0; h < kHalves; ++h) {
-          uint4* rows = reinterpret_cast<uint4*>(v + h * kHalfBytes);  // 8 x 16 bytes a row
-#pragma unroll 4
-          for (int u = every * 8 + lane; u < some * 8; u += 32) {
-            uint4 w = rows[u];
-            const uint32_t a = odd_halves(w.x), b = odd_halves(w.y), c = odd_halves(w.z),
-                           d = odd_halves(w.w);
-            if (a | b | c | d) {
-              w.x &= ~a;
-              w.y &= ~b;
-              w.z &= ~c;
-              w.w &= ~d;
-              rows[u] = w;
-              const int bit = (j - pre_chunks) * kTile + u / 8 - (it.diag + 1);
+          const uint32_t rows = v + h * kHalfBytes;  // 8 x 16 bytes a row
+          const int first = every * 8 + lane, end = some * 8;
+          // eight pieces at a time; the usual answer is that all are finite
+          for (int u = first; u < end; u += 256) {
+            uint4 w[8];
+            uint32_t odd = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] = u + 32 * e < end ? ptx::ld_shared_v4(rows + (u + 32 * e) * 16)
+                                      : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              odd |= exp_carry(w[e].x) | exp_carry(w[e].y) | exp_carry(w[e].z) | exp_carry(w[e].w);
+            if (!(odd & 0x80008000u)) continue;
+#pragma unroll 1
+            for (int x = u; x < min(end, u + 256); x += 32) {
+              uint4 y = ptx::ld_shared_v4(rows + x * 16);
+              const uint32_t a = odd_halves(y.x), b = odd_halves(y.y), c = odd_halves(y.z),
+                             d = odd_halves(y.w);
+              if (!(a | b | c | d)) continue;
+              ptx::st_shared_v4(rows + x * 16, y.x & ~a, y.y & ~b, y.z & ~c, y.w & ~d);
+              const int bit = (j - pre_chunks) * kTile + x / 8 - (it.diag + 1);
               atomicOr(&bars.odd[bit >> 5], 1u << (bit & 31));
             }
           }
-          for (int u = some * 8 + lane; u < kTile * 8; u += 32) rows[u] = make_uint4(0, 0, 0, 0);
+          for (int u = end + lane; u < kTile * 8; u += 32) ptx::st_shared_v4(rows + u * 16, 0, 0, 0, 0);
         }
         ptx::fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bars.v_ready[vs]);
     }
-  } else if (warp < 8) {
+  } else {
     // ------------------------------------------------------------ softmax
-    const int s = warp >> 2;  // query tile
-    const int r = tid & 127;  // row
+    const int s = warp >> 3;           // query tile
+    const int half = (warp >> 2) & 1;  // keys 64 half .. + 63 of each chunk
+    const int r = tid & 127;           // row
+    const int pair = 1 + s * 4 + (warp & 3);  // barrier of the two warps of 32 rows
     const int i = r / group + s * p.tile_tokens, h = hk * group + r % group;
     const int nt = s == 0 ? nt0 : it.nt, n = s == 0 ? n0 : n1;
     const bool real = i < nt && r < p.tile_tokens * group;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_col = tl + s * kTile, o_col = tl + kTmO + s * D;
+    const uint32_t s_col = tl + 64 * half, p_col = tl + kTmP + s * 64;
+    constexpr int kCols = D / 2;  // of O, for this thread
+    const uint32_t o_col = tl + kTmO + s * D + half * kCols;
     float m_run = -INFINITY, l_run = 0.f;
+    // own keys that this row sees (spare rows: all), and that every row of the warp sees
+    const int own_seen = real ? max(0, min(it.kv_n, it.diag + i + 1)) : 0x7fffffff;
+    const int own_whole = __reduce_min_sync(0xffffffffu, own_seen);
+    // After a failure the warp runs on without waiting (its partner waits for it at
+    // the pair's barriers), on whatever TMEM holds; nothing is written out then.
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      // keys of the chunk that this row sees: the first `seen` (spare rows: all)
-      int seen = kTile;
-      if (real) {
-        if (j < pre_chunks) {
-          seen = it.pre_n - j * kTile;
-        } else {
-          const int c = (j - pre_chunks) * kTile;
-          seen = min(it.kv_n, it.diag + i + 1) - c;
-        }
-        seen = min(kTile, max(0, seen));
-      }
-      const bool whole = __all_sync(0xffffffffu, seen == kTile);
-      if (!ptx::mbar_wait(&bars.s_full[s], j & 1, abort_flag, kWaitNs)) {
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (ok && !ptx::mbar_spin(bar, parity & 1, abort_flag, kWaitNs)) {
         ok = false;
-        break;
+        fail(bars, p.a.status);
       }
+      __syncwarp();
       ptx::tc_fence_after();
-      uint32_t pk[64];  // the chunk's P, pairs of bf16
-      // P = 2^(S scale - m) of the whole chunk; returns its sum
-      auto p_pass = [&](float m_ref) {
-        const float neg_m = -m_ref;
-        const uint64_t sc2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
-        const uint64_t nm2 = ptx::f2_pack(neg_m, neg_m);
-        uint64_t sum2[2] = {0ull, 0ull};
-        auto block = [&](const uint32_t (&cur)[32], int b) {
-          if (whole) {
+    };
+    for (int j = 0; j < n; ++j) {
+      // this thread's keys of the chunk: the row sees the first `seen`
+      const int at = (j < pre_chunks ? j : j - pre_chunks) * kTile + 64 * half;
+      const bool whole = at + 64 <= (j < pre_chunks ? it.pre_n : own_whole);
+      wait(&bars.s_full[s], j);
+      uint32_t c[2][32];  // the row's scores
+      ptx::tmem_ld32(s_col, c[0]);
+      ptx::tmem_ld32(s_col + 32, c[1]);
+      ptx::tmem_ld_wait(c[0]);
+      ptx::reg_barrier(c[1]);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars.s_free);
+      if (!whole) {  // masked scores become -inf under either sign of the scale
+        const uint32_t off = p.scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
+        const int seen = (j < pre_chunks ? it.pre_n : own_seen) - at;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint64_t x = ptx::f2_fma(
-                  ptx::f2_pack(__uint_as_float(cur[2 * e]), __uint_as_float(cur[2 * e + 1])), sc2,
-                  nm2);
-              float x0, x1;
-              ptx::f2_unpack(x, x0, x1);
-              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-              sum2[e & 1] = ptx::f2_add(sum2[e & 1], ptx::f2_pack(p0, p1));
-              pk[16 * b + e] = pack_bf16(p0, p1);
-            }
-          } else {
+        for (int e = 0; e < 64; ++e)
+          if (e >= seen) c[e / 32][e % 32] = off;
+      }
+      // their maximum (fmaxf drops a NaN; it comes back through ex2)
+      float mx;
+      if (p.scale_log2 >= 0.f) {
+        float t[2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int c0 = 32 * b + 2 * e;
-              const float x0 = fmaf(__uint_as_float(cur[2 * e]), p.scale_log2, neg_m);
-              const float x1 = fmaf(__uint_as_float(cur[2 * e + 1]), p.scale_log2, neg_m);
-              const float p0 = c0 < seen ? ptx::ex2(x0) : 0.f;
-              const float p1 = c0 + 1 < seen ? ptx::ex2(x1) : 0.f;
-              sum2[e & 1] = ptx::f2_add(sum2[e & 1], ptx::f2_pack(p0, p1));
-              pk[16 * b + e] = pack_bf16(p0, p1);
-            }
-          }
-        };
-        uint32_t ra[32], rb[32];
-        ptx::tmem_ld32(s_col, ra);
-        ptx::tmem_ld32(s_col + 32, rb);
-        ptx::tmem_ld_wait(ra);
-        ptx::reg_barrier(rb);
-        block(ra, 0);
-        ptx::tmem_ld32(s_col + 64, ra);
-        block(rb, 1);
-        ptx::tmem_ld32(s_col + 96, rb);
-        ptx::tmem_ld_wait(ra);
-        ptx::reg_barrier(rb);
-        block(ra, 2);
-        block(rb, 3);
-        float a, b, c, d;
-        ptx::f2_unpack(sum2[0], a, b);
-        ptx::f2_unpack(sum2[1], c, d);
-        return (a + b) + (c + d);
-      };
-      // maximum of the seen scores among the first `cols` (log2 units)
-      auto max_pass = [&](int cols) {
-        float pm[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int b = 0; b < cols / 32; ++b) {
-          uint32_t c[32];
-          ptx::tmem_ld32(s_col + 32 * b, c);
-          ptx::tmem_ld_wait(c);
+        for (int b = 0; b < 2; ++b) {
+          t[b] = __uint_as_float(c[b][0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * b + e < seen)
-              pm[e & 1] = fmaxf(pm[e & 1], __uint_as_float(c[e]) * p.scale_log2);
+          for (int e = 1; e + 1 < 32; e += 2)
+            t[b] = ptx::max3(t[b], __uint_as_float(c[b][e]), __uint_as_float(c[b][e + 1]));
         }
-        return fmaxf(pm[0], pm[1]);
-      };
-      if (j == 0) m_run = max_pass(32);
-      float sum = p_pass(m_run == -INFINITY ? 0.f : m_run);
-      // A row whose sum is too large, or that sees its first scores only now
-      // (further right than the first 32, or all of them -inf so far), takes the
-      // chunk's true maximum. TMEM accesses are warp-collective: the warp goes
-      // together, rows that need no raise keep their reference or raise it by
-      // less than 2^8. Spare rows do not vote.
-      if (__any_sync(0xffffffffu,
-                     real && (!(sum <= 256.f) || (m_run == -INFINITY && seen > 0)))) {
-        const float m_new = fmaxf(max_pass(kTile), m_run);
-        if (j > 0) {
-          // S_j is complete, so the P V before it is too: O *= 2^(m_run - m_new)
+        mx = fmaxf(ptx::max3(t[0], t[1], __uint_as_float(c[0][31])), __uint_as_float(c[1][31]));
+      } else {
+        mx = INFINITY;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) mx = fminf(mx, __uint_as_float(c[e / 32][e % 32]));
+      }
+      mx *= p.scale_log2;
+      // Raise the reference? The rows' two warps go together (TMEM accesses are
+      // warp-collective); rows that need no raise move by less than 8. Spare rows
+      // do not vote.
+      if (bar_or(pair, 64, real && mx > m_run + 8.f)) {
+        // once P's columns are free the two threads of a row swap their maxima there
+        if (j > 0) wait(&bars.pv_done[s], j - 1);
+        ptx::tmem_st1(p_col + 32 * half, __float_as_uint(mx));
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        bar_sync(pair, 64);
+        ptx::tc_fence_after();
+        const float m_new =
+            ptx::max3(m_run, mx, __uint_as_float(ptx::tmem_ld1(p_col + 32 * (1 - half))));
+        if (j > 0) {  // O *= 2^(m_run - m_new)
           const float f = m_run == -INFINITY ? 0.f : ptx::ex2(m_run - m_new);
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            ptx::tmem_ld32(o_col + q * 32, o);
+          for (int q = 0; q < kCols / 16; ++q) {
+            uint32_t o[16];
+            ptx::tmem_ld16(o_col + q * 16, o);
             ptx::tmem_ld_wait(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            ptx::tmem_st32(o_col + q * 32, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            ptx::tmem_st16(o_col + q * 16, o);
           }
           l_run *= f;
         }
         m_run = m_new;
-        sum = p_pass(m_run == -INFINITY ? 0.f : m_run);
+        ptx::tc_fence_before();
+        bar_sync(pair, 64);  // both have read before P is written
+        ptx::tc_fence_after();
       }
-      l_run += sum;
-      // every score has been read: P goes over the first 64 of S's columns
-      ptx::tmem_st32(s_col, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-      ptx::tmem_st32(s_col + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+      const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+      const uint64_t sc2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
+      const uint64_t nm2 = ptx::f2_pack(neg_m, neg_m);
+      uint64_t sum2[2] = {0ull, 0ull};
+      uint32_t pk[32];  // P, pairs of bf16
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const uint64_t x =
+            ptx::f2_fma(ptx::f2_pack(__uint_as_float(c[e / 16][2 * (e % 16)]),
+                                     __uint_as_float(c[e / 16][2 * (e % 16) + 1])),
+                        sc2, nm2);
+        float x0, x1;
+        ptx::f2_unpack(x, x0, x1);
+        const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+        sum2[e & 1] = ptx::f2_add(sum2[e & 1], ptx::f2_pack(p0, p1));
+        pk[e] = pack_bf16(p0, p1);
+      }
+      float a0, a1, a2, a3;
+      ptx::f2_unpack(sum2[0], a0, a1);
+      ptx::f2_unpack(sum2[1], a2, a3);
+      l_run += (a0 + a1) + (a2 + a3);
+      if (j > 0) wait(&bars.pv_done[s], j - 1);  // the P before has been taken
+      ptx::tmem_st32(p_col + 32 * half, pk);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
-      ptx::mbar_arrive(&bars.p_full[s]);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars.p_full[s]);
     }
-    if (ok && n > 0 && !ptx::mbar_wait(&bars.o_final[s], 0, abort_flag, kWaitNs)) ok = false;
-    if (!ok) {
-      fail(bars, p.a.status);
-    } else {
-      ptx::tc_fence_after();
-      const bool none = l_run == 0.f;  // no key seen
-      const float inv = none ? 0.f : 1.f / l_run;
-      const float lse = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+    if (n > 0) wait(&bars.pv_done[s], n - 1);
+    // The query tile's shared memory (its Q K^T are done) joins the two halves of the
+    // row's sum, then stages the rows: a warp writes whole rows (each thread its own
+    // row, 16 bytes at a time, took 8 to 19 us an item, with the rows' distance).
+    float* sums = reinterpret_cast<float*>(smem + S::stage + s * S::stage_bytes);
+    if (n > 0) sums[half * kTile + r] = l_run;
+    ok = __all_sync(0xffffffffu, ok);
+    ok = !bar_or(9 + s, 256, !ok);
+    if (ok) {
+      const float l = n > 0 ? sums[r] + sums[kTile + r] : 0.f;
+      const bool none = l == 0.f;  // no key seen
+      const float inv = none ? 0.f : 1.f / l;
       const bool part = it.slot >= 0;
-      const int64_t part_row = (int64_t)((part ? it.slot : 0) + i) * p.a.heads + h;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.O.ptr) +
-                           (int64_t)(it.q0 + i) * p.a.O.row_stride + h * p.a.O.head_stride;
-      if (real) {
+      if (real && half == 0) {
+        const float lse = none ? -INFINITY : (m_run + log2f(l)) * kLn2;
         if (part)
-          p.a.part_lse[part_row] = lse;
+          p.a.part_lse[(int64_t)(it.slot + i) * p.a.heads + h] = lse;
         else if (p.a.lse)
           p.a.lse[(int64_t)(it.q0 + i) * p.a.heads + h] = lse;
       }
+      bar_sync(9 + s, 256);  // the sums have been read
       uint32_t any_odd = 0;
       for (int w = 0; w < 8; ++w) any_odd |= bars.odd[w];
+      const uint32_t stage = base + S::stage + s * S::stage_bytes;
+      const int rows = (nt - s * p.tile_tokens) * group;  // real rows of the tile
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = 0; q < kCols / 32; ++q) {
+        const int c0 = half * kCols + q * 32;  // first channel
         uint32_t o[32];
         if (n > 0) {
-          ptx::tmem_ld32(o_col + q * 32, o);  // every lane: the load is warp-collective
+          ptx::tmem_ld32(o_col + q * 32, o);
           ptx::tmem_ld_wait(o);
         }
         float x[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = none ? 0.f : __uint_as_float(o[e]) * inv;
-        if (!real) continue;
-        if (any_odd) {
+        if (any_odd && real) {
           for (int w = 0; w < 8; ++w)
             for (uint32_t bits = bars.odd[w]; bits; bits &= bits - 1) {
               const int key = it.diag + 1 + 32 * w + __ffs(bits) - 1;
               if (key > it.diag + i) continue;
               const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.a.V.ptr) +
                                        (int64_t)(it.kv0 + key) * p.a.V.row_stride +
-                                       hk * p.a.V.head_stride + q * 32;
+                                       hk * p.a.V.head_stride + c0;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const float y = __bfloat162float(v[e]);
@@ -477,17 +529,39 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
         }
-        if (part) {
-          float4* dst = reinterpret_cast<float4*>(p.a.part_o + part_row * D + q * 32);
+        if (part) {  // 32 channels of each half at a time: rows of 256 bytes
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            ptx::st_shared_v4(stage + r * 256 + (((half * 8 + c) ^ (r & 7)) * 16),
+                              __float_as_uint(x[4 * c]), __float_as_uint(x[4 * c + 1]),
+                              __float_as_uint(x[4 * c + 2]), __float_as_uint(x[4 * c + 3]));
+          bar_sync(9 + s, 256);
+          for (int e = tid & 255; e < rows * 16; e += 256) {
+            const int rr = e >> 4, c = e & 15;
+            const uint4 v = ptx::ld_shared_v4(stage + rr * 256 + ((c ^ (rr & 7)) * 16));
+            float* to = p.a.part_o +
+                        ((int64_t)(it.slot + rr / group + s * p.tile_tokens) * p.a.heads +
+                         hk * group + rr % group) * D;
+            *reinterpret_cast<uint4*>(to + (c >> 3) * kCols + q * 32 + (c & 7) * 4) = v;
+          }
+          bar_sync(9 + s, 256);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(out + q * 32);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            dst[c] = make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
-                                pack_bf16(x[8 * c + 4], x[8 * c + 5]), pack_bf16(x[8 * c + 6], x[8 * c + 7]));
+            ptx::st_shared_v4(stage + r * (D * 2) + (((c0 / 8 + c) ^ (r & 7)) * 16),
+                              pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
+                              pack_bf16(x[8 * c + 4], x[8 * c + 5]), pack_bf16(x[8 * c + 6], x[8 * c + 7]));
+        }
+      }
+      if (!part) {
+        bar_sync(9 + s, 256);
+        for (int e = tid & 255; e < rows * (D / 8); e += 256) {
+          const int rr = e / (D / 8), c = e % (D / 8);
+          const uint4 v = ptx::ld_shared_v4(stage + rr * (D * 2) + ((c ^ (rr & 7)) * 16));
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.a.O.ptr) +
+                              (int64_t)(it.q0 + rr / group + s * p.tile_tokens) * p.a.O.row_stride +
+                              (int64_t)(hk * group + rr % group) * p.a.O.head_stride;
+          *reinterpret_cast<uint4*>(to + c * 8) = v;
         }
       }
     }
@@ -495,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmCols);
   }

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -67,19 +68,6 @@ class RotaryPlanData(ctypes.Structure):
                 ("axis", ctypes.c_uint8 * 128), ("turns", ctypes.c_uint64 * 128)]
 
 
-class RotaryTensor(ctypes.Structure):
-    _fields_ = ([("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)]
-                + [(n, ctypes.c_int64) for n in ("in_batch", "in_token", "in_head", "out_batch",
-                                                 "out_token", "out_head")]
-                + [("heads", ctypes.c_int32)])
-
-
-class RotaryCall(ctypes.Structure):
-    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("dtype", ctypes.c_int),
-                ("positions_64", ctypes.c_int32), ("positions", ctypes.c_void_p),
-                ("position_axis", ctypes.c_int64), ("position_batch", ctypes.c_int64)]
-
-
 class PackedDesc(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
@@ -93,11 +81,6 @@ class PackedPlanData(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("q_rows", ctypes.c_int64),
                 ("kv_rows", ctypes.c_int64), ("part_rows", ctypes.c_int64),
                 ("items_bytes", ctypes.c_uint64), ("ws_bytes", ctypes.c_uint64)]
-
-
-class Rows(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -417,93 +400,106 @@ class RotaryPlan:
         self.data = RotaryPlanData()
         _check(lib().tlsp_rotary_make_plan(ctypes.byref(desc), ctypes.byref(self.data)),
                "tlsp_rotary_make_plan")
+        self._at = ctypes.addressof(self.data)
         self.head_dim, self.rotary_dim, self.axes = head_dim, r, len(sec)
 
 
-def _on_device(device: torch.device):
-    """The stream to launch on: `device`'s current one (which need not be the current device)."""
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+# C structs that are filled anew for every call, as bytes: tlsp_rotary_tensor, tlsp_rotary_call,
+# tlsp_rows (a call's host time is mostly the marshalling of its arguments)
+_ROTARY_TENSOR = struct.Struct("PPqqqqqqi4x")
+_ROTARY_CALL = struct.Struct("iiiiPqq")
+_ROWS = struct.Struct("Pqq")
+_DTYPE_CODES = {torch.float32: TLSP_F32, torch.bfloat16: TLSP_BF16}
 
 
-class _Device:
-    """Makes `device` current for a launch if it is not."""
-
-    def __init__(self, device: torch.device):
-        self.guard = None
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(device: int, fn, *args):
+    """fn(*args, stream) on `device`'s current stream (`device` need not be the current one)."""
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if torch._C._cuda_getDevice() == device:
+        return fn(*args, stream)
+    with torch.cuda.device(device):
+        return fn(*args, stream)
 
 
-def _rotary_strides(x: torch.Tensor):
-    """(batch, token, head) strides of a [T, H, d] or [B, H, N, d] tensor."""
-    st = x.stride()
-    if st[-1] != 1:
+def _like(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype,
+                                                                     device=x.device)
+
+
+def _rotary_tensor(x: torch.Tensor, out: torch.Tensor, rank: int, heads: int) -> bytes:
+    st, so = x.stride(), out.stride()
+    if st[-1] != 1 or so[-1] != 1:
         raise ValueError("channels must be contiguous")
-    return (0, st[0], st[1]) if x.dim() == 3 else (st[0], st[2], st[1])
+    if rank == 3:
+        return _ROTARY_TENSOR.pack(x.data_ptr(), out.data_ptr(), 0, st[0], st[1], 0, so[0], so[1],
+                                   heads)
+    return _ROTARY_TENSOR.pack(x.data_ptr(), out.data_ptr(), st[0], st[2], st[1], so[0], so[2],
+                               so[1], heads)
 
 
-def _rotary_tensor(x: torch.Tensor, out: torch.Tensor) -> RotaryTensor:
-    return RotaryTensor(x.data_ptr(), out.data_ptr(), *_rotary_strides(x), *_rotary_strides(out),
-                        x.shape[1])
+def _rotary_out(x: torch.Tensor, o: torch.Tensor, dev: int):
+    if o.shape != x.shape or o.dtype != x.dtype or o.get_device() != dev:
+        raise ValueError("out must match the input's shape, type and device")
+    if any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
+        raise ValueError("out must not be a broadcast tensor")
 
 
 def _rotary(Q, K, positions, plan: RotaryPlan, out, backward: int):
-    many = K is not None
-    xs = (Q, K) if many else (Q,)
-    if Q.dim() not in (3, 4):
-        raise ValueError("tensors are [tokens, heads, head_dim] or [batch, heads, tokens, head_dim]")
-    batch, tokens = (1, Q.shape[0]) if Q.dim() == 3 else (Q.shape[0], Q.shape[2])
-    dev = Q.device
-    if dev.type != "cuda":
-        raise ValueError("tensors must live on the CUDA device")
-    code = _dtype_code(Q.dtype)
-    for x in xs:
-        if x.dim() != Q.dim() or x.dtype != Q.dtype or x.device != dev:
-            raise ValueError("queries and keys must have the same rank, type and device")
-        if x.shape[-1] != plan.head_dim or x.shape[1] < 1:
-            raise ValueError(f"expected heads of {plan.head_dim} channels, got {tuple(x.shape)}")
-        if (x.shape[0] if x.dim() == 3 else x.shape[2]) != tokens or (x.dim() == 4
-                                                                      and x.shape[0] != batch):
-            raise ValueError("queries and keys must have the same tokens")
-    if out is None:
-        outs = tuple(torch.empty(x.shape, dtype=x.dtype, device=dev) for x in xs)
+    shape = Q.shape
+    rank = len(shape)
+    if rank == 3:
+        batch, (tokens, heads, d) = 1, shape
+    elif rank == 4:
+        batch, heads, tokens, d = shape
     else:
-        outs = tuple(out) if many else (out,)
-        if len(outs) != len(xs):
-            raise ValueError("out must be one tensor per input")
-        for x, o in zip(xs, outs):
-            if o.shape != x.shape or o.dtype != x.dtype or o.device != dev:
-                raise ValueError("out must match the input's shape, type and device")
-            if any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
-                raise ValueError("out must not be a broadcast tensor")
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != dev:
+        raise ValueError("tensors are [tokens, heads, head_dim] or [batch, heads, tokens, head_dim]")
+    dev, dtype = Q.get_device(), Q.dtype
+    if dev < 0:
+        raise ValueError("tensors must live on the CUDA device")
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if d != plan.head_dim or heads < 1:
+        raise ValueError(f"expected heads of {plan.head_dim} channels, got {tuple(shape)}")
+    if K is not None:
+        if K.dtype != dtype or K.get_device() != dev or K.dim() != rank:
+            raise ValueError("queries and keys must have the same rank, type and device")
+        k_heads = K.shape[1]
+        if K.shape != ((tokens, k_heads, d) if rank == 3 else (batch, k_heads, tokens, d)) or \
+                k_heads < 1:
+            raise ValueError(f"queries and keys must have the same tokens and channels, got "
+                             f"{tuple(shape)} and {tuple(K.shape)}")
+    p_type, p_shape, p_stride = positions.dtype, positions.shape, positions.stride()
+    if (p_type != torch.int32 and p_type != torch.int64) or positions.get_device() != dev:
         raise ValueError("positions must be int32 or int64 on the tensors' device")
-    shape, lead = tuple(positions.shape), (() if plan.axes == 1 else (plan.axes,))
-    if shape == lead + (tokens,):
+    lead = () if plan.axes == 1 else (plan.axes,)
+    if p_shape == lead + (tokens,):
         p_batch = 0
-    elif Q.dim() == 4 and shape == lead + (batch, tokens):
-        p_batch = positions.stride(-2)
+    elif rank == 4 and p_shape == lead + (batch, tokens):
+        p_batch = p_stride[-2]
     else:
         raise ValueError(f"positions must be {lead + (tokens,)} (or with the batch before the "
-                         f"tokens), got {shape}")
-    if tokens > 1 and positions.stride(-1) != 1:
+                         f"tokens), got {tuple(p_shape)}")
+    if tokens > 1 and p_stride[-1] != 1:
         raise ValueError("positions must be contiguous along the tokens")
-    call = RotaryCall(batch, tokens, code, positions.dtype == torch.int64, positions.data_ptr(),
-                      positions.stride(0) if lead else 0, p_batch)
-    ts = [_rotary_tensor(x, o) for x, o in zip(xs, outs)]
-    with _Device(dev):
-        _check(lib().tlsp_rotary(ctypes.byref(plan.data), ctypes.byref(call), ctypes.byref(ts[0]),
-                                 ctypes.byref(ts[1]) if many else None, backward,
-                                 _on_device(dev)), "tlsp_rotary")
-    return outs if many else outs[0]
+    if out is None:
+        q_out, k_out = _like(Q), None if K is None else _like(K)
+    elif K is None:
+        q_out, k_out = out, None
+        _rotary_out(Q, q_out, dev)
+    else:
+        if len(out) != 2:
+            raise ValueError("out must be one tensor per input")
+        q_out, k_out = out
+        _rotary_out(Q, q_out, dev)
+        _rotary_out(K, k_out, dev)
+    rc = _launch(dev, lib().tlsp_rotary, plan._at,
+                 _ROTARY_CALL.pack(batch, tokens, code, p_type == torch.int64,
+                                   positions.data_ptr(), p_stride[0] if lead else 0, p_batch),
+                 _rotary_tensor(Q, q_out, rank, heads),
+                 None if K is None else _rotary_tensor(K, k_out, rank, k_heads), backward)
+    _check(rc, "tlsp_rotary")
+    return q_out if K is None else (q_out, k_out)
 
 
 def rotary(Q: torch.Tensor, K: Optional[torch.Tensor], positions: torch.Tensor, plan: RotaryPlan,
@@ -580,6 +576,7 @@ class PackedPlan:
         used = max(self.data.items_bytes, 16)
         # a blocking copy: the table is in place for every stream when this returns
         self.items = torch.frombuffer(table, dtype=torch.uint8)[:used].to(device)
+        self._at, self._dev = ctypes.addressof(self.data), device.index
         self._made_on = torch.cuda.current_stream(device).cuda_stream
 
     def workspace(self) -> "Workspace":
@@ -592,57 +589,57 @@ def _packed_rows(t: Optional[torch.Tensor], what: str, rows: int, heads: int, pl
         if rows:
             raise ValueError(f"{what} is missing")
         return None
-    if t.dim() != 3 or t.shape[0] < rows or t.shape[1] != heads or t.shape[2] != plan.head_dim:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < rows or shape[1] != heads or shape[2] != plan.head_dim:
         raise ValueError(f"{what} must be [>= {rows}, {heads}, {plan.head_dim}], "
-                         f"got {tuple(t.shape)}")
-    if t.dtype != plan.dtype or t.device != plan.device:
+                         f"got {tuple(shape)}")
+    if t.dtype != plan.dtype or t.get_device() != plan._dev:
         raise ValueError(f"{what} must be {plan.dtype} on {plan.device}")
     s0, s1, s2 = t.stride()
     if s2 != 1:
         raise ValueError(f"{what}: channels must be contiguous")
-    return ctypes.byref(Rows(t.data_ptr(), s0, s1))
+    return _ROWS.pack(t.data_ptr(), s0, s1)
 
 
 def _packed(Q, Kp, Vp, K, V, plan: PackedPlan, ws: Workspace, scale, out, lse):
-    what = "tlsp_prefix_attention" if plan.prefix_len else "tlsp_packed_attention"
-    q_rows, h, hk = plan.q_rows, plan.heads, plan.kv_heads
-    dev = plan.device
+    q_rows, kv_rows, h, hk, dev = plan.q_rows, plan.kv_rows, plan.heads, plan.kv_heads, plan._dev
     q = _packed_rows(Q, "Q", q_rows, h, plan)
-    k = _packed_rows(K, "K", plan.kv_rows, hk, plan)
-    v = _packed_rows(V, "V", plan.kv_rows, hk, plan)
+    k = _packed_rows(K, "K", kv_rows, hk, plan)
+    v = _packed_rows(V, "V", kv_rows, hk, plan)
     if out is None:
-        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        out = _like(Q)
         if Q.shape[0] > q_rows:
             out[q_rows:].zero_()
     o = _packed_rows(out, "out", q_rows, h, plan)
     lse_ptr = None
     if lse is not None:
-        if lse.dtype != torch.float32 or lse.device != dev or lse.dim() != 2 or \
+        if lse.dtype != torch.float32 or lse.get_device() != dev or lse.dim() != 2 or \
                 lse.shape[0] < q_rows or lse.shape[1] != h or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous fp32 [>= {q_rows}, {h}] on {dev}")
+            raise ValueError(f"lse must be contiguous fp32 [>= {q_rows}, {h}] on {plan.device}")
         lse_ptr = lse.data_ptr()
-    if ws.buf.device != dev:
-        raise ValueError(f"the workspace must live on {dev}")
+    if ws.buf.get_device() != dev:
+        raise ValueError(f"the workspace must live on {plan.device}")
     if scale is None:
         scale = 0.0
     elif scale == 0.0:
         raise ValueError("scale must not be 0")
-    with _Device(dev):
+    if torch._C._cuda_getCurrentRawStream(dev) != plan._made_on and \
+            not torch.cuda.is_current_stream_capturing():
+        # their memory is not reused before this call is done
         stream = torch.cuda.current_stream(dev)
-        if stream.cuda_stream != plan._made_on and not torch.cuda.is_current_stream_capturing():
-            plan.items.record_stream(stream)  # its memory is not reused before this call is done
-            ws.buf.record_stream(stream)
-        st, items = ctypes.c_void_p(stream.cuda_stream), plan.items.data_ptr()
-        data = ctypes.byref(plan.data)
-        if plan.prefix_len:
-            kp = _packed_rows(Kp, "K_prefix", plan.prefix_len, hk, plan)
-            vp = _packed_rows(Vp, "V_prefix", plan.prefix_len, hk, plan)
-            code = lib().tlsp_prefix_attention(data, items, q, kp, vp, k, v, o, lse_ptr, scale,
-                                               ws.ptr, ws.nbytes, st)
-        else:
-            code = lib().tlsp_packed_attention(data, items, q, k, v, o, lse_ptr, scale, ws.ptr,
-                                               ws.nbytes, st)
-    _check(code, what)
+        plan.items.record_stream(stream)
+        ws.buf.record_stream(stream)
+    items, at = plan.items.data_ptr(), plan._at
+    if plan.prefix_len:
+        kp = _packed_rows(Kp, "K_prefix", plan.prefix_len, hk, plan)
+        vp = _packed_rows(Vp, "V_prefix", plan.prefix_len, hk, plan)
+        rc = _launch(dev, lib().tlsp_prefix_attention, at, items, q, kp, vp, k, v, o, lse_ptr,
+                     scale, ws.buf.data_ptr(), ws.nbytes)
+        _check(rc, "tlsp_prefix_attention")
+    else:
+        rc = _launch(dev, lib().tlsp_packed_attention, at, items, q, k, v, o, lse_ptr, scale,
+                     ws.buf.data_ptr(), ws.nbytes)
+        _check(rc, "tlsp_packed_attention")
     return out
 
 
