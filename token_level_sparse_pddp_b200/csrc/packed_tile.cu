@@ -615,22 +615,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sc2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
         const uint64_t nm2 = ptx::f2_pack(neg_m, neg_m);
         uint64_t sum2[2] = {0ull, 0ull};
+        uint32_t pk[2][16];  // P, pairs of bf16
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {  // 32 keys at a time: P takes 16 registers
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t y = ptx::f2_fma(
-                ptx::f2_pack(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1])), sc2, nm2);
-            float y0, y1;
-            ptx::f2_unpack(y, y0, y1);
-            const float p0 = ptx::ex2(y0), p1 = ptx::ex2(y1);
-            sum2[e & 1] = ptx::f2_add(sum2[e & 1], ptx::f2_pack(p0, p1));
-            pk[e] = pack_bf16(p0, p1);
-          }
-          if (b == 0 && c > c0) wait(&bars.pv_done[s], c - 1);  // the P before has been taken
-          ptx::tmem_st16(p_col + 16 * b, pk);
+        for (int e = 0; e < 32; ++e) {
+          const uint64_t y =
+              ptx::f2_fma(ptx::f2_pack(__uint_as_float(x[e / 16][2 * (e % 16)]),
+                                       __uint_as_float(x[e / 16][2 * (e % 16) + 1])),
+                          sc2, nm2);
+          float y0, y1;
+          ptx::f2_unpack(y, y0, y1);
+          const float p0 = ptx::ex2(y0), p1 = ptx::ex2(y1);
+          sum2[e & 1] = ptx::f2_add(sum2[e & 1], ptx::f2_pack(p0, p1));
+          pk[e / 16][e % 16] = pack_bf16(p0, p1);
         }
+        if (c > c0) wait(&bars.pv_done[s], c - 1);  // the P before has been taken
+        ptx::tmem_st16(p_col, pk[0]);
+        ptx::tmem_st16(p_col + 16, pk[1]);
         float a0, a1, a2, a3;
         ptx::f2_unpack(sum2[0], a0, a1);
         ptx::f2_unpack(sum2[1], a2, a3);
