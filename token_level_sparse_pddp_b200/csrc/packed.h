@@ -31,7 +31,7 @@ static_assert(sizeof(MergeItem) == 32, "item table layout");
 
 constexpr int kTokenRows = 16;    // rows (tokens x heads of a group) of a token item
 constexpr int kSimtTileRows = 64;  // rows of a tile item, fp32
-constexpr int kMergeTokens = 4;   // tokens of a merge item
+constexpr int kMergeTokens = 1;   // tokens of a merge item
 
 constexpr int kTcRows = 128;       // rows of one of the two query tiles of a bf16 tile item
 
@@ -66,10 +66,42 @@ __device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t
          t.diag <= t.kv_n && (t.slot < 0 || (int64_t)t.slot + t.nt <= a.part_rows);
 }
 
+// Launches a kernel that may start while the kernel before it in the stream is still
+// finishing (programmatic dependent launch). Each block of it has to execute
+// wait_for_previous() before it reads what that kernel wrote, and before it exits.
+template <class... Params, class... Args>
+int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st,
+                 Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const int rc = check_launch();
+  if (e == cudaSuccess) return rc;
+  set_last_cuda_error(e);
+  return TLSP_ERR_CUDA;
+}
+// Until the kernel before has completed and its writes are visible.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the kernel behind start once every block of this one has said so.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // packed_tile.cu: tile items on the tensor cores (bf16)
 int packed_tile(const PackedArgs& a, cudaStream_t st);
 // packed_token.cu: token items (bf16)
-int packed_token(const PackedArgs& a, cudaStream_t st);
+// `after`: another kernel of the call precedes it in the stream
+int packed_token(const PackedArgs& a, bool after, cudaStream_t st);
 // packed_simt.cu: both kinds of items (fp32)
 int packed_simt(const PackedArgs& a, cudaStream_t st);
 // packed_merge.cu: merge items

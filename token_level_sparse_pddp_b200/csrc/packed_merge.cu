@@ -1,18 +1,60 @@
-// Joins the partial results of rows whose keys were split over several items.
+// Joins the partial results of rows whose keys were split over several items:
+//   O = sum_p e^(lse_p - lse) O_p with lse = log sum_p e^(lse_p).
+//
+// One warp per row. Bound by latency (a few dependent reads of L2), so it starts
+// while the kernel before is finishing, reads its item meanwhile, and then has
+// eight parts' rows in flight with their log partitions. fp32 throughout; parts are
+// added in their order, so results do not depend on which CTA was first.
 #include "packed.h"
 
 namespace tlsp {
 namespace {
 
-// Partial results of a row over its key ranges: O = sum_p e^(lse_p - lse) O_p
-// with lse = log sum_p e^(lse_p). One warp per row.
+constexpr int kWarps = 4;
+constexpr int kAhead = 8;  // parts in flight
+
+template <int D>
+struct Row;  // a lane's channels of a row
+template <>
+struct Row<128> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void add(float w, float (&acc)[4]) const {
+    acc[0] = fmaf(w, v.x, acc[0]);
+    acc[1] = fmaf(w, v.y, acc[1]);
+    acc[2] = fmaf(w, v.z, acc[2]);
+    acc[3] = fmaf(w, v.w, acc[3]);
+  }
+};
+template <>
+struct Row<64> {
+  float2 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+  __device__ __forceinline__ void add(float w, float (&acc)[2]) const {
+    acc[0] = fmaf(w, v.x, acc[0]);
+    acc[1] = fmaf(w, v.y, acc[1]);
+  }
+};
+
+__device__ __forceinline__ void store(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store(float* p, const float (&x)[2]) {
+  *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+}
+template <int E>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(p + e) = __floats2bfloat162_rn(x[e], x[e + 1]);
+}
+
 template <class T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kWarps)
     packed_merge_kernel(const __grid_constant__ PackedArgs p) {
   const MergeItem it = p.merges[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + warp;
-  if (row >= it.nt * p.heads) return;
+  const int row = blockIdx.y * kWarps + warp;
   const int i = row / p.heads, h = row % p.heads;
   const int parts = it.a_parts + it.b_parts;
   const bool ok = it.q0 >= 0 && it.nt >= 1 && (int64_t)it.q0 + it.nt <= p.q_rows &&
@@ -22,63 +64,61 @@ __global__ void __launch_bounds__(256)
                                           p.part_rows) &&
                   (it.b_parts == 0 || it.b_slot + (int64_t)(it.b_parts - 1) * it.b_stride + it.nt <=
                                           p.part_rows);
+  wait_for_previous();
   if (!ok) {
-    if (lane == 0) record_status(p.status, TLSP_ERR_DEVICE_ASSERT);
+    if (threadIdx.x == 0) record_status(p.status, TLSP_ERR_DEVICE_ASSERT);
     return;
   }
+  if (i >= it.nt) return;
   auto part_row = [&](int q) {
     const int64_t slot = q < it.a_parts
                              ? it.a_slot + (int64_t)q * it.a_stride
                              : it.b_slot + (int64_t)(q - it.a_parts) * it.b_stride;
     return (slot + i) * p.heads + h;
   };
-  float mx = -INFINITY;
-  for (int q = lane; q < parts; q += 32) mx = fmaxf(mx, p.part_lse[part_row(q)]);
-  mx = warp_max(mx);
-  const float m_use = mx == -INFINITY ? 0.f : mx;
   constexpr int E = D / 32;
   float acc[E] = {};
-  float sum = 0.f;
-  for (int q0 = 0; q0 < parts; q0 += 32) {
-    // a part that saw no key (lse -inf) has weight 0 and O = 0
-    const float w_lane = q0 + lane < parts ? expf(p.part_lse[part_row(q0 + lane)] - m_use) : 0.f;
+  float m = -INFINITY, sum = 0.f;  // running maximum of the log partitions
+  for (int q0 = 0; q0 < parts; q0 += 32) {  // 32 parts: a lane each for the weights
     const int n = min(32, parts - q0);
-#pragma unroll 4
-    for (int q = 0; q < n; ++q) {
-      const float w = __shfl_sync(0xffffffffu, w_lane, q);
-      const float* o = p.part_o + part_row(q0 + q) * D + lane * E;
-      sum += w;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-      }
+    const float lse = lane < n ? p.part_lse[part_row(q0 + lane)] : -INFINITY;
+    Row<D> rows[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      if (e < n) rows[e].load(p.part_o + part_row(q0 + e) * D + lane * E);
+    const float to = fmaxf(m, warp_max(lse)), use = to == -INFINITY ? 0.f : to;
+    const float f = m == -INFINITY ? 0.f : expf(m - use);
+    m = to;
+    sum *= f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+    // a part that saw no key (-inf) has weight 0, and O = 0
+    const float w_lane = expf(lse - use);
+    sum += warp_sum(w_lane);
+    for (int b = 0; b < n; b += kAhead) {
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (b + e < n) {
+          rows[e].add(__shfl_sync(0xffffffffu, w_lane, b + e), acc);
+          if (b + e + kAhead < n) rows[e].load(p.part_o + part_row(q0 + b + e + kAhead) * D + lane * E);
+        }
     }
   }
   const bool none = sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
-  T* o = static_cast<T*>(p.O.ptr) + (it.q0 + i) * p.O.row_stride + h * p.O.head_stride + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = from_f32<T>(acc[e] * inv);
+  for (int e = 0; e < E; ++e) acc[e] *= inv;
+  store(static_cast<T*>(p.O.ptr) + (it.q0 + i) * p.O.row_stride + h * p.O.head_stride + lane * E, acc);
   if (p.lse && lane == 0)
-    p.lse[(int64_t)(it.q0 + i) * p.heads + h] = none ? -INFINITY : m_use + logf(sum);
+    p.lse[(int64_t)(it.q0 + i) * p.heads + h] = none ? -INFINITY : m + logf(sum);
 }
 
 template <class T>
 int merge(const PackedArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)a.n_merges, (unsigned)ceil_div((int64_t)kMergeTokens * a.heads, 8));
+  const dim3 grid((unsigned)a.n_merges, (unsigned)ceil_div((int64_t)kMergeTokens * a.heads, kWarps));
   if (grid.y > 65535) return TLSP_ERR_UNSUPPORTED;
-  if (a.d == 128)
-    packed_merge_kernel<T, 128><<<grid, 256, 0, st>>>(a);
-  else
-    packed_merge_kernel<T, 64><<<grid, 256, 0, st>>>(a);
-  return check_launch();
+  return launch_after(a.d == 128 ? packed_merge_kernel<T, 128> : packed_merge_kernel<T, 64>, grid,
+                      32 * kWarps, 0, st, a);
 }
 
 }  // namespace

@@ -54,16 +54,26 @@ int64_t steps_of(const PackedItem& t) {
   return ceil_div(t.pre_n, kChunk) + ceil_div(t.kv_n, kChunk);
 }
 
-// Time of the tile items, in steps, on kSms CTAs taking them longest first,
-// when none may exceed `most` steps; `fixed` steps are charged per item for
-// its prologue and epilogue, as many again for a part's merge.
-double makespan(const std::vector<int64_t>& steps, int kv_heads, int64_t most, double fixed) {
+// An item's steps, and what one of them costs.
+struct Load {
+  int64_t steps;
+  double cost;
+  // parts of at most `most` cost, each of one step at least
+  int64_t parts(double most) const {
+    return std::max<int64_t>(1, std::min<int64_t>(steps, (int64_t)std::ceil((double)steps * cost / most)));
+  }
+};
+
+// Time of tile items on kSms CTAs taking them longest first when each is cut into
+// parts of at most `most`, and `fixed` is spent on starting and finishing each.
+double makespan(const std::vector<Load>& loads, int kv_heads, double most, double fixed) {
   std::vector<double> jobs;
-  for (int64_t s : steps) {
-    const int64_t parts = std::max<int64_t>(1, ceil_div(s, most));
+  for (const Load& l : loads) {
+    const int64_t parts = l.parts(most);
     for (int64_t i = 0; i < parts; ++i)
       for (int h = 0; h < kv_heads; ++h)
-        jobs.push_back((double)(s * (i + 1) / parts - s * i / parts) + fixed * (parts > 1 ? 2 : 1));
+        jobs.push_back((double)(l.steps * (i + 1) / parts - l.steps * i / parts) * l.cost +
+                       fixed * (parts > 1 ? 1.5 : 1));
   }
   std::sort(jobs.begin(), jobs.end(), std::greater<double>());
   std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
@@ -106,11 +116,9 @@ class Planner {
         int e = s;  // a run of such sequences: their queries are consecutive
         while (e < d_.num_seqs && few_[e]) ++e;
         const int64_t q0 = q0_[s], n = q0_[e - 1] + q_lens_[e - 1] - q0;
-        const int64_t tiles = ceil_div(n, tile_tokens_);
-        for (int64_t i = 0; i < tiles; ++i) {  // equal shares
-          const int64_t a = n * i / tiles, b = n * (i + 1) / tiles;
-          shared.push_back({(int32_t)(q0 + a), (int32_t)(b - a), 0, 0, 0, d_.prefix_len, 0, 0});
-        }
+        for (int64_t i = 0; i < n; i += tile_tokens_)
+          shared.push_back({(int32_t)(q0 + i), (int32_t)std::min<int64_t>(tile_tokens_, n - i), 0, 0, 0,
+                            d_.prefix_len, 0, 0});
         s = e;
       }
     }
@@ -124,9 +132,9 @@ class Planner {
         ++i;
       }
     }
-    const int64_t most = tile_split(whole, shared);
+    const double most = tile_split(whole, shared);
     for (const PackedItem& t : whole) {
-      const int64_t parts = std::max<int64_t>(1, ceil_div(steps_of(t), most));
+      const int64_t parts = load_of(t).parts(most);
       if (parts == 1) {
         tiles.push_back(t);
         continue;
@@ -144,7 +152,7 @@ class Planner {
       pieces.push_back({t.q0, t.nt, base, parts});
     };
     for (const PackedItem& t : shared)
-      add_shared(t, std::max<int64_t>(1, ceil_div(steps_of(t), most)), tiles);
+      add_shared(t, load_of(t).parts(most), tiles);
     for (const PackedItem& t : shared_tokens)
       add_shared(t, std::max<int64_t>(1, ceil_div(t.pre_n, range)), tokens);
     std::sort(pieces.begin(), pieces.end(),
@@ -267,33 +275,53 @@ class Planner {
                         (int32_t)b_parts, (int32_t)b_stride});
   }
 
-  // Most steps of a tile item. With many more items than SMs they stay whole;
-  // else the split of least estimated time is taken.
-  int64_t tile_split(const std::vector<PackedItem>& whole, const std::vector<PackedItem>& shared) {
-    std::vector<int64_t> steps;
-    int64_t total = 0, longest = 1;
+  // A step of an item with one query tile takes 0.6 of one with two (measured with
+  // d = 128: 1.0 us and 1.7 us).
+  Load load_of(const PackedItem& t) const {
+    const bool one_tile = d_.dtype == TLSP_BF16 && 2 * t.nt <= tile_tokens_;
+    return {steps_of(t), one_tile ? 0.6 : 1.0};
+  }
+
+  // Most cost of a tile item. With many more items than SMs they stay whole; else the
+  // split of least estimated time is taken, among those that fill the SMs evenly a few
+  // times over. Starting and finishing an item takes about three steps (5 us).
+  double tile_split(const std::vector<PackedItem>& whole, const std::vector<PackedItem>& shared) {
+    std::vector<Load> loads;
+    double longest = 1, total = 0;
     for (const auto* v : {&whole, &shared})
       for (const PackedItem& t : *v) {
-        steps.push_back(steps_of(t));
-        total += steps.back();
-        longest = std::max(longest, steps.back());
+        loads.push_back(load_of(t));
+        const double all = (double)loads.back().steps * loads.back().cost;
+        total += all;
+        longest = std::max(longest, all);
       }
-    if (steps.empty()) return 1;
-    const int64_t jobs = (int64_t)steps.size() * d_.kv_heads;
-    const double mean = (double)total * d_.kv_heads / kSms;
+    if (loads.empty()) return 1;
+    const int64_t jobs = (int64_t)loads.size() * d_.kv_heads;
+    const double mean = total * d_.kv_heads / kSms;
     if (jobs > 16 * kSms && longest < mean / 2) return longest;
     const double fixed = 3.0;
-    int64_t best = longest;
-    double least = makespan(steps, d_.kv_heads, longest, fixed);
-    for (int k = 1; k <= 6; ++k) {
-      const int64_t most = std::max<int64_t>(4, (int64_t)std::ceil(mean / k));
-      if (most >= longest) continue;
-      const double t = makespan(steps, d_.kv_heads, most, fixed);
+    double best = longest, least = makespan(loads, d_.kv_heads, longest, fixed);
+    auto try_split = [&](double most) {
+      if (most >= longest) return;
+      const double t = makespan(loads, d_.kv_heads, most, fixed);
       if (t < 0.97 * least) {
         least = t;
         best = most;
       }
+    };
+    for (int rounds = 1; rounds <= 4; ++rounds) {
+      if (jobs > (int64_t)rounds * kSms) continue;
+      double lo = 4, hi = longest;  // least cost that gives at most `rounds` items an SM
+      for (int i = 0; i < 12; ++i) {
+        const double mid = 0.5 * (lo + hi);
+        int64_t n = 0;
+        for (const Load& l : loads) n += l.parts(mid);
+        (n * d_.kv_heads <= (int64_t)rounds * kSms ? hi : lo) = mid;
+      }
+      try_split(hi);
     }
+    if (jobs > kSms)  // long items among many: cut to a share of the mean
+      for (int k = 1; k <= 4; ++k) try_split(std::max(4.0, mean / k));
     return best;
   }
 
@@ -406,7 +434,7 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   cudaStream_t st = (cudaStream_t)stream;
   if (bf16) {
     if (a.n_tiles > 0) TLSP_TRY(packed_tile(a, st));
-    if (a.n_tokens > 0) TLSP_TRY(packed_token(a, st));
+    if (a.n_tokens > 0) TLSP_TRY(packed_token(a, a.n_tiles > 0, st));
   } else {
     TLSP_TRY(packed_simt(a, st));
   }

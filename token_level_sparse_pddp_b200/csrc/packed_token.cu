@@ -39,6 +39,7 @@ struct Smem {
 struct TokenParams {
   PackedArgs a;
   float scale_log2;
+  bool after;  // launched behind the tile items
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -62,8 +63,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int hk = blockIdx.x % p.a.kv_heads;
   const PackedItem it = p.a.tokens[blockIdx.x / p.a.kv_heads];
   const int group = p.a.group;
+  let_next_start();
   if (!item_ok(p.a, it, kTokenRows / group)) {
     if (threadIdx.x == 0) record_status(p.a.status, TLSP_ERR_DEVICE_ASSERT);
+    if (p.after) wait_for_previous();
     return;
   }
   if (threadIdx.x == 0) s_odd = 0;
@@ -283,21 +286,25 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (c == 0) p.a.part_lse[row] = lse;
     }
   }
+  // nothing here depends on the tile items; what follows this kernel may
+  if (p.after) wait_for_previous();
 }
 
 template <int D>
-int launch(const PackedArgs& a, cudaStream_t st) {
-  const TokenParams p{a, a.scale * 1.4426950408889634f};
+int launch(const PackedArgs& a, bool after, cudaStream_t st) {
+  const TokenParams p{a, a.scale * 1.4426950408889634f, after};
   auto kernel = packed_token_kernel<D>;
   TLSP_TRY(ensure_smem_limit((const void*)kernel, (int)Smem<D>::bytes));
-  kernel<<<(unsigned)((int64_t)a.n_tokens * a.kv_heads), kThreads, Smem<D>::bytes, st>>>(p);
+  const dim3 grid((unsigned)((int64_t)a.n_tokens * a.kv_heads));
+  if (after) return launch_after(kernel, grid, kThreads, (int)Smem<D>::bytes, st, p);
+  kernel<<<grid, kThreads, Smem<D>::bytes, st>>>(p);
   return check_launch();
 }
 
 }  // namespace
 
-int packed_token(const PackedArgs& a, cudaStream_t st) {
-  return a.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
+int packed_token(const PackedArgs& a, bool after, cudaStream_t st) {
+  return a.d == 128 ? launch<128>(a, after, st) : launch<64>(a, after, st);
 }
 
 }  // namespace tlsp
