@@ -30,14 +30,17 @@ struct MergeItem {
 static_assert(sizeof(MergeItem) == 32, "item table layout");
 
 constexpr int kTokenRows = 16;    // rows (tokens x heads of a group) of a token item
-constexpr int kSimtTileRows = 64;  // rows of a tile item, fp32
 constexpr int kMergeTokens = 1;   // tokens of a merge item
 
 constexpr int kTcRows = 128;       // rows of one of the two query tiles of a bf16 tile item
 
-// Most tokens of a tile item: whole groups of `group` rows per query tile.
+// Rows of a tile item, fp32: 32 (twice as many items as with 64, for balance; half of
+// the 64 rows' K and V reuse, which the CUDA cores do not need), or one token's.
+inline int simt_tile_rows(int group) { return group <= 32 ? 32 : 64; }
+
+// Most tokens of a tile item: whole groups of `group` rows (per query tile).
 inline int tile_tokens(bool bf16, int group) {
-  return bf16 ? 2 * (kTcRows / group) : kSimtTileRows / group;
+  return bf16 ? 2 * (kTcRows / group) : simt_tile_rows(group) / group;
 }
 
 struct PackedArgs {

@@ -23,6 +23,7 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
 constexpr int kSms = 148;  // planning assumes a B200
+constexpr int kSimtCtas = 3;  // fp32 tile items that share an SM
 constexpr int kChunk = 128;  // keys a tile item takes at a time
 
 int validate_desc(const tlsp_packed_desc* d) {
@@ -64,9 +65,9 @@ struct Load {
   }
 };
 
-// Time of tile items on kSms CTAs taking them longest first when each is cut into
+// Time of tile items on `slots` CTAs taking them longest first when each is cut into
 // parts of at most `most`, and `fixed` is spent on starting and finishing each.
-double makespan(const std::vector<Load>& loads, int kv_heads, double most, double fixed) {
+double makespan(const std::vector<Load>& loads, int kv_heads, double most, double fixed, int slots) {
   std::vector<double> jobs;
   for (const Load& l : loads) {
     const int64_t parts = l.parts(most);
@@ -80,7 +81,7 @@ double makespan(const std::vector<Load>& loads, int kv_heads, double most, doubl
   double last = 0;
   for (double j : jobs) {
     double at = 0;
-    if ((int)ends.size() == kSms) {
+    if ((int)ends.size() == slots) {
       at = ends.top();
       ends.pop();
     }
@@ -284,7 +285,8 @@ class Planner {
 
   // Most cost of a tile item. With many more items than SMs they stay whole; else the
   // split of least estimated time is taken, among those that fill the SMs evenly a few
-  // times over. Starting and finishing an item takes about three steps (5 us).
+  // times over. Starting and finishing an item takes about three steps of 1.7 us (fp32:
+  // 0.7 of 4 us, with three CTAs on an SM).
   double tile_split(const std::vector<PackedItem>& whole, const std::vector<PackedItem>& shared) {
     std::vector<Load> loads;
     double longest = 1, total = 0;
@@ -297,31 +299,32 @@ class Planner {
       }
     if (loads.empty()) return 1;
     const int64_t jobs = (int64_t)loads.size() * d_.kv_heads;
-    const double mean = total * d_.kv_heads / kSms;
-    if (jobs > 16 * kSms && longest < mean / 2) return longest;
-    const double fixed = 3.0;
-    double best = longest, least = makespan(loads, d_.kv_heads, longest, fixed);
+    const int slots = d_.dtype == TLSP_BF16 ? kSms : kSimtCtas * kSms;
+    const double mean = total * d_.kv_heads / slots;
+    if (jobs > 16 * slots && longest < mean / 2) return longest;
+    const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7, shortest = d_.dtype == TLSP_BF16 ? 4.0 : 1.0;
+    double best = longest, least = makespan(loads, d_.kv_heads, longest, fixed, slots);
     auto try_split = [&](double most) {
       if (most >= longest) return;
-      const double t = makespan(loads, d_.kv_heads, most, fixed);
+      const double t = makespan(loads, d_.kv_heads, most, fixed, slots);
       if (t < 0.97 * least) {
         least = t;
         best = most;
       }
     };
     for (int rounds = 1; rounds <= 4; ++rounds) {
-      if (jobs > (int64_t)rounds * kSms) continue;
-      double lo = 4, hi = longest;  // least cost that gives at most `rounds` items an SM
+      if (jobs > (int64_t)rounds * slots) continue;
+      double lo = shortest, hi = longest;  // least cost that gives at most `rounds` items an SM
       for (int i = 0; i < 12; ++i) {
         const double mid = 0.5 * (lo + hi);
         int64_t n = 0;
         for (const Load& l : loads) n += l.parts(mid);
-        (n * d_.kv_heads <= (int64_t)rounds * kSms ? hi : lo) = mid;
+        (n * d_.kv_heads <= (int64_t)rounds * slots ? hi : lo) = mid;
       }
       try_split(hi);
     }
-    if (jobs > kSms)  // long items among many: cut to a share of the mean
-      for (int k = 1; k <= 4; ++k) try_split(std::max(4.0, mean / k));
+    if (2 * jobs > slots)  // long items among many: cut to a share of the mean
+      for (int k = 1; k <= 4; ++k) try_split(std::max(shortest, mean / k));
     return best;
   }
 
