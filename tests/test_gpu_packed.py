@@ -177,6 +177,29 @@ def test_masked_keys_have_no_influence(T, dtype, prefix):
     assert torch.isfinite(O[first][:100]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_sequences_that_share_an_item(T, d):
+    """A few tokens of several sequences behind one prefix: each sees its own keys only, whatever
+    the others' hold."""
+    q, kv, starts = [1, 2, 0, 3, 1], [40, 17, 6, 3, 0], [100, 0, 60, 200, 0]
+    Q, K, V, Kp, Vp = inputs(q, kv, 4, 2, d, BF16, 333, kv_rows=260)
+    keep = torch.zeros(260, dtype=torch.bool, device="cuda")
+    for s, m in zip(starts, kv):
+        keep[s:s + m] = True
+    K[~keep], V[~keep] = float("nan"), float("inf")
+    V[100 + 39, :, 3] = float("inf")         # seen by the first sequence
+    V[5, 0, 7], V[6, 0, 7] = float("inf"), float("-inf")
+    V[16, 1, 20] = float("nan")              # the second sequence's last key
+    V[201, :, 1] = float("-inf")             # the fourth's second token on
+    plan = T.PackedPlan(q, kv, 4, 2, d, BF16, True, 333, starts)
+    ws = plan.workspace()
+    O, lse = attend(T, Q, K, V, Kp, Vp, plan, ws)
+    assert ws.status() == T.TLSP_OK
+    ref = Ref(Q, K, V, q, kv, starts, True, Kp, Vp)
+    ref.check(O, lse)
+    assert torch.isnan(ref.O).any() and torch.isinf(ref.O).any()
+
+
 def test_rows_behind_the_last_sequence(T):
     q, kv = [40, 1], [40, 300]
     Q, K, V, _, _ = inputs(q, kv, 4, 2, 128, BF16, rows=60, kv_rows=400)
@@ -278,6 +301,8 @@ def test_refusals(T):
     Q, K, V, Kp, Vp = inputs(q, kv, 4, 2, 128, BF16, 5)
     plan, pplan = T.PackedPlan(q, kv, 4, 2, 128), T.PackedPlan(q, kv, 4, 2, 128, prefix_len=5)
     ws, small = pplan.workspace(), T.Workspace.status_only()
+    many = inputs([1] * 40, [9] * 40, 4, 2, 128, BF16, 5)       # shared tiles: partial results
+    mplan = T.PackedPlan([1] * 40, [9] * 40, 4, 2, 128, prefix_len=5)
     before = T.launch_count()
     bad = [
         lambda: T.packed_attention(Q[:3], K, V, plan, ws),
@@ -304,7 +329,8 @@ def test_refusals(T):
             f()
             pytest.fail(f"call {i} was not refused")
     status = [
-        (T.TLSP_ERR_WORKSPACE, lambda: T.prefix_attention(Q, Kp, Vp, K, V, pplan, small)),
+        (T.TLSP_ERR_WORKSPACE, lambda: T.prefix_attention(many[0], many[3], many[4], many[1], many[2],
+                                                          mplan, small)),
         (T.TLSP_ERR_INVALID_ARG, lambda: T.packed_attention(Q, K[:, :1].expand(12, 2, 128), V, plan, ws)),
         (T.TLSP_ERR_INVALID_ARG, lambda: T.PackedPlan([-1], [1], 4, 2, 128)),
         (T.TLSP_ERR_INVALID_ARG, lambda: T.PackedPlan([1], [1], 4, 3, 128)),

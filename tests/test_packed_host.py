@@ -49,8 +49,32 @@ def make(T, q, kv, heads=4, kv_heads=2, d=128, dtype=1, causal=1, prefix=0, star
     assert L.tlsp_packed_make_plan(ctypes.byref(desc), aq, akv, ast, buf, data.items_bytes,
                                    ctypes.byref(data)) == T.TLSP_OK
     table = np.frombuffer(bytes(buf)[:data.items_bytes], dtype=np.int32).reshape(-1, 8)
-    n1, n2 = data.tile_items, data.tile_items + data.token_items
-    return data, table[:n1], table[n1:n2], table[n2:]
+    n1 = data.tile_items
+    n2 = n1 + data.token_items
+    n3 = n2 + data.token_segments
+    assert len(table) == n3 + data.merge_items and data.cluster in (1, 2, 4, 8)
+    return data, table[:n1], token_work(table[n1:n2], table[n2:n3], dtype), table[n3:]
+
+
+def token_work(tokens, segments, dtype):
+    """Token items as rows (q0, nt, kv0, kv_n, pre0, pre_n, diag, slot, counts): one for each
+    segment (bf16; those of sequences that share an item cover part of its tokens), or as they
+    are (fp32). `counts`: whether the row stands for the item's result."""
+    if dtype == 0:
+        assert len(segments) == 0
+        return [list(t) + [1] for t in tokens.tolist()]
+    out, used = [], []
+    for q0, nt, seg0, nseg, slot, *_ in tokens.tolist():
+        assert 0 <= nseg <= 32
+        used += range(seg0, seg0 + nseg)
+        out.append([q0, nt, 0, 0, 0, 0, 0, slot, 1])
+        for k0, n, tok0, ntok, diag, prefix, *_ in segments[seg0:seg0 + nseg].tolist():
+            assert n > 0 and tok0 >= 0 and ntok >= 1 and tok0 + ntok <= nt
+            out.append([q0 + tok0, ntok] + ([0, 0, k0, n, 0] if prefix else [k0, n, 0, 0, diag])
+                       + [-1, 0])
+            assert not prefix or (tok0, ntok) == (0, nt)
+    assert sorted(used) == list(range(len(segments)))
+    return out
 
 
 def check_cover(T, q, kv, heads, kv_heads, d, dtype, causal, prefix, starts=None):
@@ -69,7 +93,8 @@ def check_cover(T, q, kv, heads, kv_heads, d, dtype, causal, prefix, starts=None
     slots = {}                        # partial row -> token
     direct = [0] * rows
     for kind, table in (("tile", tiles), ("token", tokens)):
-        for q0, nt, kv0, kv_n, pre0, pre_n, diag, slot in table.tolist():
+        rows_of = table if kind == "token" else [t + [1] for t in table.tolist()]
+        for q0, nt, kv0, kv_n, pre0, pre_n, diag, slot, counts in rows_of:
             assert nt >= 1 and q0 >= 0 and q0 + nt <= rows
             assert nt * g <= (16 if kind == "token" else 256)
             assert 0 <= pre0 and pre0 + pre_n <= prefix and pre_n >= 0 and kv_n >= 0 and kv0 >= 0
@@ -82,6 +107,8 @@ def check_cover(T, q, kv, heads, kv_heads, d, dtype, causal, prefix, starts=None
                     own[t].append((kv0, seen))
                 if pre_n:
                     pre[t].append((pre0, pre_n))
+                if not counts:
+                    continue
                 if slot < 0:
                     direct[t] += 1
                 else:
@@ -146,7 +173,7 @@ def test_plan_covers_random_batches(T):
 def test_long_caches_are_split(T):
     """A single token behind a long cache is shared out over many CTAs."""
     data, tiles, tokens, merges = make(T, [1], [60000], heads=12, kv_heads=4)
-    assert len(tiles) == 0 and len(tokens) * 4 >= 100 and len(merges) == 1
+    assert len(tiles) == 0 and data.token_items * data.cluster * 4 >= 100 and len(merges) == 1
     data, tiles, tokens, merges = make(T, [100], [60000], heads=12, kv_heads=4)
     assert len(tokens) == 0 and len(tiles) * 4 >= 100
 

@@ -20,6 +20,23 @@ struct PackedItem {
 };
 static_assert(sizeof(PackedItem) == 32, "item table layout");
 
+// Token items of bf16 plans: tokens q0 .. q0 + nt - 1 (up to kTokenRows rows) against
+// the keys of nseg segments. slot as above.
+struct TokenItem {
+  int32_t q0, nt;
+  int32_t seg0, nseg;
+  int32_t slot, pad[3];
+};
+// Keys k0 .. k0 + n - 1 of the prefix, which all of the item's tokens see, or of K:
+// then tokens tok0 + i, i < ntok, see the first min(n, diag + i + 1) of them, the others
+// none.
+struct TokenSegment {
+  int32_t k0, n;
+  int32_t tok0, ntok;
+  int32_t diag, prefix, pad[2];
+};
+static_assert(sizeof(TokenItem) == 32 && sizeof(TokenSegment) == 32, "item table layout");
+
 // Tokens q0 .. q0 + nt - 1: partial rows a_slot + p * a_stride + i for p <
 // a_parts, then the same with b.
 struct MergeItem {
@@ -32,6 +49,8 @@ static_assert(sizeof(MergeItem) == 32, "item table layout");
 constexpr int kTokenRows = 16;    // rows (tokens x heads of a group) of a token item
 constexpr int kMergeTokens = 1;   // tokens of a merge item
 
+constexpr int kMaxSegments = 32;  // of a token item: its tokens' sequences and the prefix
+constexpr int kMaxCluster = 8;    // CTAs that share a token item (portable cluster size)
 constexpr int kTcRows = 128;       // rows of one of the two query tiles of a bf16 tile item
 
 // Rows of a tile item, fp32: 32 (twice as many items as with 64, for balance; half of
@@ -45,9 +64,12 @@ inline int tile_tokens(bool bf16, int group) {
 
 struct PackedArgs {
   const PackedItem* tiles;
-  const PackedItem* tokens;
+  const PackedItem* tokens;    // fp32
+  const TokenItem* token_items;  // bf16: the same entries
+  const TokenSegment* segments;
   const MergeItem* merges;
-  int n_tiles, n_tokens, n_merges;
+  int n_tiles, n_tokens, n_segments, n_merges;
+  int cluster;  // CTAs of a token item (bf16)
   int heads, kv_heads, group, d;
   int64_t q_rows, kv_rows, prefix_len, part_rows;
   tlsp_rows Q, K, V, Kp, Vp, O;
@@ -69,22 +91,30 @@ __device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t
          t.diag <= t.kv_n && (t.slot < 0 || (int64_t)t.slot + t.nt <= a.part_rows);
 }
 
-// Launches a kernel that may start while the kernel before it in the stream is still
-// finishing (programmatic dependent launch). Each block of it has to execute
-// wait_for_previous() before it reads what that kernel wrote, and before it exits.
+// Launches a kernel in clusters of `cluster` CTAs. `after`: it may start while the kernel
+// before it in the stream is still finishing (programmatic dependent launch); each block
+// of it then has to execute wait_for_previous() before it reads what that kernel wrote,
+// and before it exits.
 template <class... Params, class... Args>
-int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st,
-                 Args... args) {
+int launch_ex(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster, bool after,
+              cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attrs[2] = {};
+  if (after) {
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attrs[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+    attrs[cfg.numAttrs].val.clusterDim.y = 1;
+    attrs[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attrs;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   const int rc = check_launch();
   if (e == cudaSuccess) return rc;

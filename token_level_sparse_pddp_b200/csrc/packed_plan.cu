@@ -6,8 +6,8 @@
 //   tile items   up to a tile's rows of one sequence against its keys (and the
 //                prefix), or the rows of many short sequences against the
 //                prefix, which is then read once for all of them;
-//   token items  up to 16 rows (a few tokens of one sequence) against a range
-//                of keys: memory-bound, split until the GPU is full;
+//   token items  up to 16 rows (the tokens of one sequence, or of several with the
+//                prefix) against their keys: memory-bound, split until the GPU is full;
 //   merge items  tokens whose keys were split.
 #include <algorithm>
 #include <cmath>
@@ -23,6 +23,8 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
 constexpr int kSms = 148;  // planning assumes a B200
+constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
+constexpr int kTokenBlock = 16;        // keys a warp of a token item takes at a time
 constexpr int kSimtCtas = 3;  // fp32 tile items that share an SM
 constexpr int kChunk = 128;  // keys a tile item takes at a time
 
@@ -144,46 +146,16 @@ class Planner {
       split(t, parts, base, tiles);
       add_merge(t.q0, t.nt, base, parts, t.nt, 0, 0, 0);
     }
-    // Few-query sequences: own keys in token items, split over the GPU.
-    const int64_t range = token_range(shared_tokens);
     std::vector<Piece> pieces;  // where the prefix results of each token lie
-    auto add_shared = [&](const PackedItem& t, int64_t parts, std::vector<PackedItem>& to) {
-      const int64_t base = take_slots(parts * t.nt);
-      split(t, parts, base, to);
+    for (const PackedItem& t : shared) {
+      const int64_t parts = load_of(t).parts(most), base = take_slots(parts * t.nt);
+      split(t, parts, base, tiles);
       pieces.push_back({t.q0, t.nt, base, parts});
-    };
-    for (const PackedItem& t : shared)
-      add_shared(t, load_of(t).parts(most), tiles);
-    for (const PackedItem& t : shared_tokens)
-      add_shared(t, std::max<int64_t>(1, ceil_div(t.pre_n, range)), tokens);
-    std::sort(pieces.begin(), pieces.end(),
-              [](const Piece& a, const Piece& b) { return a.q0 < b.q0; });
-    size_t at = 0;
-    for (int s = 0; s < d_.num_seqs; ++s) {
-      if (!few_[s] || q_lens_[s] == 0) continue;
-      const int32_t n = q_lens_[s], m = kv_lens_[s];
-      const int64_t diag = d_.causal ? (int64_t)m - n : m;
-      const int64_t parts = d_.prefix_len > 0 && m == 0 ? 0 : std::max<int64_t>(1, ceil_div(m, range));
-      const PackedItem t = {(int32_t)q0_[s], n, (int32_t)kv0_[s], m, 0, 0, clamp_diag(diag, m), -1};
-      if (parts == 1 && d_.prefix_len == 0) {
-        tokens.push_back(t);
-        continue;
-      }
-      const int64_t base = take_slots(parts * n);
-      if (parts > 0) split(t, parts, base, tokens);
-      if (d_.prefix_len == 0) {
-        add_merge(t.q0, n, base, parts, n, 0, 0, 0);
-        continue;
-      }
-      int64_t q = q0_[s];
-      while (q < q0_[s] + n) {  // the pieces that hold its prefix results
-        while (pieces[at].q0 + pieces[at].nt <= q) ++at;
-        const Piece& p = pieces[at];
-        const int64_t to = std::min<int64_t>(q0_[s] + n, p.q0 + p.nt);
-        add_merge(q, to - q, p.slot + (q - p.q0), p.parts, p.nt, base + (q - q0_[s]), parts, n);
-        q = to;
-      }
     }
+    if (d_.dtype == TLSP_BF16)
+      plan_tokens(shared_tokens, pieces);
+    else
+      plan_tokens_simt(shared_tokens, pieces);
     if (part_rows_ > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
     // longest first: the grid is handed out in this order
     auto longer = [](const PackedItem& a, const PackedItem& b) {
@@ -191,14 +163,21 @@ class Planner {
     };
     std::stable_sort(tiles.begin(), tiles.end(), longer);
     std::stable_sort(tokens.begin(), tokens.end(), longer);
+    std::stable_sort(token_items.begin(), token_items.end(), [&](const TokenItem& a, const TokenItem& b) {
+      return keys_of(a) > keys_of(b);
+    });
     const int64_t most_items =
-        std::max({tiles.size(), tokens.size(), merges.size()}) * (uint64_t)d_.kv_heads;
+        std::max({tiles.size(), tokens.size(), token_items.size() * (size_t)cluster, merges.size()}) *
+        (uint64_t)d_.kv_heads;
     if (most_items > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
     return TLSP_OK;
   }
 
   std::vector<PackedItem> tiles, tokens;
+  std::vector<TokenItem> token_items;
+  std::vector<TokenSegment> segments;
   std::vector<MergeItem> merges;
+  int cluster = 1;
   int64_t q_rows = 0, kv_rows = 0;
   int64_t part_rows() const { return part_rows_; }
 
@@ -328,24 +307,181 @@ class Planner {
     return best;
   }
 
-  // Keys of a token item: small enough to give every SM its CTAs in one go
-  // where the keys are few, about three rounds of them where they are many.
-  int64_t token_range(const std::vector<PackedItem>& shared_tokens) const {
+  // Keys of a token item of the fp32 kernel: small enough to give every SM its CTAs in
+  // one go where the keys are few, about three rounds of them where they are many.
+  int64_t simt_range(const std::vector<PackedItem>& shared_tokens) const {
     std::vector<int64_t> lens;
-    int64_t total = 0;
     for (int s = 0; s < d_.num_seqs; ++s)
       if (few_[s] && q_lens_[s] > 0 && kv_lens_[s] > 0) lens.push_back(kv_lens_[s]);
     for (const PackedItem& t : shared_tokens) lens.push_back(t.pre_n);
-    for (int64_t l : lens) total += l;
-    const int64_t slots = 2 * kSms;  // CTAs resident at once
-    auto ctas = [&](int64_t range) {
-      int64_t n = 0;
-      for (int64_t l : lens) n += ceil_div(l, range);
-      return n * d_.kv_heads;
-    };
     int64_t range = kChunk;
-    while (range < 2048 && ctas(range) > slots) range += kChunk;
+    while (range < 2048 && parts_of(lens, range) * d_.kv_heads > kTokenSlots) range += kChunk;
     return range;
+  }
+
+  static int64_t parts_of(const std::vector<int64_t>& lens, int64_t range) {
+    int64_t n = 0;
+    for (int64_t l : lens) n += std::max<int64_t>(1, ceil_div(l, range));
+    return n;
+  }
+
+  // Merge entries of a few-query sequence: its prefix results lie in `pieces`, its own
+  // in `parts` partial rows from `base`.
+  void merge_sequence(int s, int64_t base, int64_t parts, const std::vector<Piece>& pieces,
+                      size_t& at) {
+    const int32_t n = q_lens_[s];
+    if (d_.prefix_len == 0) {
+      add_merge(q0_[s], n, base, parts, n, 0, 0, 0);
+      return;
+    }
+    int64_t q = q0_[s];
+    while (q < q0_[s] + n) {  // the pieces that hold its prefix results
+      while (pieces[at].q0 + pieces[at].nt <= q) ++at;
+      const Piece& p = pieces[at];
+      const int64_t to = std::min<int64_t>(q0_[s] + n, p.q0 + p.nt);
+      add_merge(q, to - q, p.slot + (q - p.q0), p.parts, p.nt, base + (q - q0_[s]), parts, n);
+      q = to;
+    }
+  }
+
+  void plan_tokens_simt(const std::vector<PackedItem>& shared_tokens, std::vector<Piece>& pieces) {
+    const int64_t range = simt_range(shared_tokens);
+    for (const PackedItem& t : shared_tokens) {
+      const int64_t parts = std::max<int64_t>(1, ceil_div(t.pre_n, range));
+      const int64_t base = take_slots(parts * t.nt);
+      split(t, parts, base, tokens);
+      pieces.push_back({t.q0, t.nt, base, parts});
+    }
+    std::sort(pieces.begin(), pieces.end(),
+              [](const Piece& a, const Piece& b) { return a.q0 < b.q0; });
+    size_t at = 0;
+    for (int s = 0; s < d_.num_seqs; ++s) {
+      if (!few_[s] || q_lens_[s] == 0) continue;
+      const int32_t n = q_lens_[s], m = kv_lens_[s];
+      const int64_t parts = d_.prefix_len > 0 && m == 0 ? 0 : std::max<int64_t>(1, ceil_div(m, range));
+      const PackedItem t = {(int32_t)q0_[s], n, (int32_t)kv0_[s], m, 0, 0, own_diag(s), -1};
+      if (parts == 1 && d_.prefix_len == 0) {
+        tokens.push_back(t);
+        continue;
+      }
+      const int64_t base = take_slots(parts * n);
+      if (parts > 0) split(t, parts, base, tokens);
+      merge_sequence(s, base, parts, pieces, at);
+    }
+  }
+
+  int32_t own_diag(int s) const {
+    return clamp_diag(d_.causal ? (int64_t)kv_lens_[s] - q_lens_[s] : kv_lens_[s], kv_lens_[s]);
+  }
+
+  // bf16: an item's keys are shared by the CTAs of a cluster, which join their results
+  // through each other's shared memory: a batch of a few sequences takes one launch.
+  // Only what a cluster cannot hold (long caches of very few sequences) is cut into
+  // several items and merged, and what shares the prefix by tile items.
+  void plan_tokens(const std::vector<PackedItem>& shared_tokens, std::vector<Piece>& pieces) {
+    struct Draft {
+      TokenItem item;
+      std::vector<TokenSegment> segs;
+      int64_t keys = 0;
+      bool piece = false;  // prefix results alone, of tokens whose own keys come elsewhere
+      int seq = -1;        // own keys alone of this sequence
+      int64_t parts = 0, base = -1;
+    };
+    std::vector<Draft> drafts;
+    auto add = [](Draft& d, const TokenSegment& s) {
+      if (s.n == 0) return;
+      d.segs.push_back(s);
+      d.keys += s.n;
+    };
+    std::vector<char> taken((size_t)d_.num_seqs, 0);
+    for (const PackedItem& t : shared_tokens) {
+      Draft d;
+      d.item = {t.q0, t.nt, 0, 0, -1, {}};
+      add(d, {t.pre0, t.pre_n, 0, t.nt, t.pre_n, 1, {}});
+      // with all its tokens' own keys, if no sequence has tokens elsewhere too
+      const int first = sequence_of(t.q0), last = sequence_of((int64_t)t.q0 + t.nt - 1);
+      d.piece = q0_[first] < t.q0 || q0_[last] + q_lens_[last] > t.q0 + t.nt;
+      for (int s = first; s <= last && !d.piece; ++s) {
+        if (q_lens_[s] == 0) continue;
+        taken[(size_t)s] = 1;
+        add(d, {(int32_t)kv0_[s], kv_lens_[s], (int32_t)(q0_[s] - t.q0), q_lens_[s], own_diag(s), 0, {}});
+      }
+      drafts.push_back(std::move(d));
+    }
+    for (int s = 0; s < d_.num_seqs; ++s) {
+      if (!few_[s] || q_lens_[s] == 0 || taken[(size_t)s]) continue;
+      Draft d;
+      d.item = {(int32_t)q0_[s], q_lens_[s], 0, 0, -1, {}};
+      add(d, {(int32_t)kv0_[s], kv_lens_[s], 0, q_lens_[s], own_diag(s), 0, {}});
+      if (d_.prefix_len > 0) d.seq = s;
+      drafts.push_back(std::move(d));
+    }
+    if (drafts.empty()) return;
+    // CTAs of an item: as many as fill the GPU in one go, with 64 keys each at least
+    std::vector<int64_t> lens;
+    int64_t longest = 0, total = 0;
+    for (const Draft& d : drafts) {
+      lens.push_back(d.keys);
+      longest = std::max(longest, d.keys);
+      total += d.keys;
+    }
+    const int64_t jobs = (int64_t)drafts.size() * d_.kv_heads;
+    while (cluster < kMaxCluster && jobs * 2 * cluster <= kTokenSlots && longest > 64 * cluster)
+      cluster *= 2;
+    // Items of more keys than a cluster's share are cut: where the GPU would stay empty,
+    // to fill it; else at twice the mean keys of a place for a CTA, 512 at least.
+    const int64_t mean = ceil_div(total * d_.kv_heads, kTokenSlots);
+    int64_t range = std::max<int64_t>(512, 2 * mean) * cluster;
+    if (jobs * cluster * 2 <= kTokenSlots) {
+      range = 256 * cluster;
+      while (parts_of(lens, range) * d_.kv_heads * cluster > kTokenSlots) range += 32 * cluster;
+    }
+    for (Draft& d : drafts) {
+      d.parts = d.seq >= 0 && d.keys == 0 ? 0 : std::max<int64_t>(1, ceil_div(d.keys, range));
+      const bool merged = d.parts > 1 || d.seq >= 0 || d.piece;
+      if (merged) d.base = take_slots(d.parts * d.item.nt);
+      for (int64_t p = 0; p < d.parts; ++p) {  // keys [a, b) of the concatenated segments
+        const int64_t a = d.keys * p / d.parts / kTokenBlock * kTokenBlock;
+        const int64_t b =
+            p + 1 == d.parts ? d.keys : d.keys * (p + 1) / d.parts / kTokenBlock * kTokenBlock;
+        TokenItem t = d.item;
+        t.seg0 = (int32_t)segments.size();
+        t.slot = merged ? (int32_t)(d.base + p * t.nt) : -1;
+        int64_t from = 0;
+        for (const TokenSegment& s : d.segs) {
+          const int64_t lo = std::max<int64_t>(a - from, 0), hi = std::min<int64_t>(b - from, s.n);
+          from += s.n;
+          if (lo >= hi) continue;
+          TokenSegment x = s;
+          x.k0 = (int32_t)(s.k0 + lo);
+          x.n = (int32_t)(hi - lo);
+          x.diag = clamp_diag((int64_t)s.diag - lo, x.n);
+          segments.push_back(x);
+        }
+        t.nseg = (int32_t)segments.size() - t.seg0;
+        token_items.push_back(t);
+      }
+      if (d.piece)
+        pieces.push_back({d.item.q0, d.item.nt, d.base, d.parts});
+      else if (merged && d.seq < 0)
+        add_merge(d.item.q0, d.item.nt, d.base, d.parts, d.item.nt, 0, 0, 0);
+    }
+    std::sort(pieces.begin(), pieces.end(),
+              [](const Piece& a, const Piece& b) { return a.q0 < b.q0; });
+    size_t at = 0;
+    for (const Draft& d : drafts)
+      if (d.seq >= 0) merge_sequence(d.seq, d.base, d.parts, pieces, at);
+  }
+
+  int sequence_of(int64_t token) const {  // the one that holds it
+    auto it = std::upper_bound(q0_.begin(), q0_.end(), token);
+    return (int)(it - q0_.begin()) - 1;
+  }
+
+  int64_t keys_of(const TokenItem& t) const {
+    int64_t n = 0;
+    for (int i = 0; i < t.nseg; ++i) n += segments[(size_t)(t.seg0 + i)].n;
+    return n;
   }
 
   tlsp_packed_desc d_;
@@ -382,7 +518,7 @@ tlsp_rows tidy(const tlsp_rows* r, int64_t rows, int heads, int d) {
 int validate_packed(const tlsp_packed_plan* p) {
   if (!p) return TLSP_ERR_INVALID_ARG;
   TLSP_TRY(validate_desc(&p->desc));
-  if (p->tile_items < 0 || p->token_items < 0 || p->merge_items < 0 || p->q_rows < 0 ||
+  if (p->tile_items < 0 || p->token_items < 0 || p->token_segments < 0 || p->merge_items < 0 || p->q_rows < 0 ||
       p->kv_rows < 0 || p->part_rows < 0 || p->q_rows > 0x7ffffeffLL || p->kv_rows > 0x7ffffeffLL)
     return TLSP_ERR_INVALID_ARG;
   return TLSP_OK;
@@ -410,7 +546,11 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   PackedArgs a{};
   a.tiles = static_cast<const PackedItem*>(items);
   a.tokens = a.tiles + plan->tile_items;
-  a.merges = reinterpret_cast<const MergeItem*>(a.tokens + plan->token_items);
+  a.token_items = reinterpret_cast<const TokenItem*>(a.tokens);
+  a.segments = reinterpret_cast<const TokenSegment*>(a.tokens + plan->token_items);
+  a.merges = reinterpret_cast<const MergeItem*>(a.segments + plan->token_segments);
+  a.n_segments = plan->token_segments;
+  a.cluster = plan->cluster;
   a.n_tiles = plan->tile_items;
   a.n_tokens = plan->token_items;
   a.n_merges = plan->merge_items;
@@ -463,13 +603,16 @@ int tlsp_packed_make_plan(const tlsp_packed_desc* desc, const int32_t* q_lens,
     tlsp_packed_plan out{};
     out.desc = *desc;
     out.tile_items = (int32_t)p.tiles.size();
-    out.token_items = (int32_t)p.tokens.size();
+    out.token_items = (int32_t)(p.tokens.size() + p.token_items.size());
+    out.token_segments = (int32_t)p.segments.size();
+    out.cluster = p.cluster;
     out.merge_items = (int32_t)p.merges.size();
     out.q_rows = p.q_rows;
     out.kv_rows = p.kv_rows;
     out.part_rows = p.part_rows();
     out.items_bytes =
-        sizeof(PackedItem) * (p.tiles.size() + p.tokens.size()) + sizeof(MergeItem) * p.merges.size();
+        sizeof(PackedItem) * (p.tiles.size() + p.tokens.size() + p.token_items.size() +
+                              p.segments.size() + p.merges.size());
     out.ws_bytes = ws_layout(out).total;
     *plan = out;
     if (items_bytes < out.items_bytes || (out.items_bytes > 0 && !items)) return TLSP_ERR_WORKSPACE;
@@ -480,6 +623,8 @@ int tlsp_packed_make_plan(const tlsp_packed_desc* desc, const int32_t* q_lens,
     };
     put(p.tiles.data(), sizeof(PackedItem) * p.tiles.size());
     put(p.tokens.data(), sizeof(PackedItem) * p.tokens.size());
+    put(p.token_items.data(), sizeof(TokenItem) * p.token_items.size());
+    put(p.segments.data(), sizeof(TokenSegment) * p.segments.size());
     put(p.merges.data(), sizeof(MergeItem) * p.merges.size());
   } catch (...) {  // out of host memory
     return TLSP_ERR_UNSUPPORTED;
