@@ -41,6 +41,48 @@ int device_sm_count();
 // device; the attribute call is made once per (kernel, device, size).
 int ensure_smem_limit(const void* fn, int bytes);
 
+// ----------------------------------------------------------------- dependent launches
+
+// Launches a kernel, in clusters of `cluster` CTAs, that may start while the kernel before
+// it in the stream is still finishing (programmatic dependent launch): its launch and
+// first instructions then cost no time of their own (1 to 2 us a kernel, back to back).
+// Each block has to execute wait_for_previous() before it touches memory that kernels
+// before may write or read, and before it exits.
+template <class... Params, class... Args>
+int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster,
+                     cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = attrs;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const int rc = check_launch();
+  if (e == cudaSuccess) return rc;
+  set_last_cuda_error(e);
+  return TLSP_ERR_CUDA;
+}
+// Until the kernel before has completed and its writes are visible.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the kernel behind start once every block of this one has said so.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- device side
 
 // Device status word: the first error wins, later ones are dropped.

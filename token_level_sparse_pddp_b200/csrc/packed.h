@@ -91,45 +91,6 @@ __device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t
          t.diag <= t.kv_n && (t.slot < 0 || (int64_t)t.slot + t.nt <= a.part_rows);
 }
 
-// Launches a kernel in clusters of `cluster` CTAs. `after`: it may start while the kernel
-// before it in the stream is still finishing (programmatic dependent launch); each block
-// of it then has to execute wait_for_previous() before it reads what that kernel wrote,
-// and before it exits.
-template <class... Params, class... Args>
-int launch_ex(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster, bool after,
-              cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attrs[2] = {};
-  if (after) {
-    attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attrs[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
-    attrs[cfg.numAttrs].val.clusterDim.y = 1;
-    attrs[cfg.numAttrs++].val.clusterDim.z = 1;
-  }
-  cfg.attrs = attrs;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  const int rc = check_launch();
-  if (e == cudaSuccess) return rc;
-  set_last_cuda_error(e);
-  return TLSP_ERR_CUDA;
-}
-// Until the kernel before has completed and its writes are visible.
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-// Lets the kernel behind start once every block of this one has said so.
-__device__ __forceinline__ void let_next_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // packed_tile.cu: tile items on the tensor cores (bf16)
 int packed_tile(const PackedArgs& a, cudaStream_t st);
 // packed_token.cu: token items (bf16)

@@ -117,8 +117,8 @@ template <class T>
 int merge(const PackedArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)a.n_merges, (unsigned)ceil_div((int64_t)kMergeTokens * a.heads, kWarps));
   if (grid.y > 65535) return TLSP_ERR_UNSUPPORTED;
-  return launch_ex(a.d == 128 ? packed_merge_kernel<T, 128> : packed_merge_kernel<T, 64>, grid,
-                   32 * kWarps, 0, 1, true, st, a);
+  return launch_dependent(a.d == 128 ? packed_merge_kernel<T, 128> : packed_merge_kernel<T, 64>, grid,
+                          32 * kWarps, 0, 1, st, a);
 }
 
 }  // namespace

@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(Config<D, BM, RM>::threads)
   float* sP = sV + kBN * LD;
   const PackedItem it = items[blockIdx.x / p.kv_heads];
   const int hk = blockIdx.x % p.kv_heads;
+  wait_for_previous();
   if (!item_ok(p, it, BM / p.group)) {
     if (threadIdx.x == 0) record_status(p.status, TLSP_ERR_DEVICE_ASSERT);
     return;
@@ -270,8 +271,8 @@ int launch(const PackedArgs& a, const PackedItem* items, int n, cudaStream_t st)
   using C = Config<D, BM, RM>;
   auto kernel = packed_simt_kernel<D, BM, RM>;
   TLSP_TRY(ensure_smem_limit((const void*)kernel, C::bytes));
-  kernel<<<(unsigned)((int64_t)n * a.kv_heads), C::threads, C::bytes, st>>>(a, items);
-  return check_launch();
+  return launch_dependent(kernel, dim3((unsigned)((int64_t)n * a.kv_heads)), C::threads, C::bytes, 1, st, a,
+                          items);
 }
 
 template <int D>

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&p.tmK);
     ptx::prefetch_tmap(&p.tmV);
   }
+  wait_for_previous();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -817,8 +818,8 @@ int launch(const PackedArgs& a, cudaStream_t st) {
   TLSP_TRY(kv_map(&p.tmVp, a.Vp, a.prefix_len, a.kv_heads, D));
   auto kernel = a.part_rows > 0 ? packed_tile_kernel<D, true> : packed_tile_kernel<D, false>;
   TLSP_TRY(ensure_smem_limit((const void*)kernel, (int)Smem<D>::bytes));
-  kernel<<<(unsigned)((int64_t)a.n_tiles * a.kv_heads), kThreads, Smem<D>::bytes, st>>>(p);
-  return check_launch();
+  return launch_dependent(kernel, dim3((unsigned)((int64_t)a.n_tiles * a.kv_heads)), kThreads,
+                          (int)Smem<D>::bytes, 1, st, p);
 }
 
 }  // namespace

@@ -46,7 +46,7 @@ struct Smem {
 struct TokenParams {
   PackedArgs a;
   float scale_log2;
-  bool after;  // launched behind the tile items
+  bool after;  // launched behind the tile items, on whose results nothing here depends
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -126,9 +126,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   ok = __all_sync(0xffffffffu, ok);  // the same for every warp of the cluster
   let_next_start();
+  // (what the tile items' kernel waited for is done when this one starts behind it)
+  if (!p.after || !ok) wait_for_previous();
   if (!ok) {
     if (threadIdx.x == 0) record_status(p.a.status, TLSP_ERR_DEVICE_ASSERT);
-    if (p.after) wait_for_previous();
     return;
   }
   int first = (sg.n + kKeys - 1) / kKeys, blocks;
@@ -448,8 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
-  // nothing here depends on the tile items; what follows this kernel may
-  if (p.after) wait_for_previous();
+  if (p.after) wait_for_previous();  // what follows this kernel may depend on them
 }
 
 template <int D>
@@ -458,7 +458,7 @@ int launch(const PackedArgs& a, bool after, cudaStream_t st) {
   auto kernel = packed_token_kernel<D>;
   TLSP_TRY(ensure_smem_limit((const void*)kernel, (int)Smem<D>::bytes));
   const dim3 grid((unsigned)((int64_t)a.n_tokens * a.kv_heads * a.cluster));
-  return launch_ex(kernel, grid, kThreads, (int)Smem<D>::bytes, a.cluster, after, st, p);
+  return launch_dependent(kernel, grid, kThreads, (int)Smem<D>::bytes, a.cluster, st, p);
 }
 
 }  // namespace

@@ -129,10 +129,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   const int64_t rest = id / p.units;
   const int part = (int)(rest % p.head_split);
   const int64_t row = rest / p.head_split;
-  if (row >= (int64_t)p.batch * p.tokens) return;
+  if (row >= (int64_t)p.batch * p.tokens) {
+    wait_for_previous();
+    return;
+  }
   const int b = (int)(row / p.tokens), n = (int)(row % p.tokens);
   const int R = p.plan.rotary_dim;
   const bool turned = u < p.rot_units;
+  wait_for_previous();
 
   float c[V], s[V];
   int c0, c1;
@@ -229,12 +233,11 @@ int launch(RotaryParams& p, const tlsp_rotary_call& call, bool two, cudaStream_t
   p.head_split = (int)split;
   const int64_t blocks = ceil_div(rows * p.units * split, kThreads);
   if (blocks > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
-  auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, kThreads, 0, st>>>(p); };
-  if (wide)
-    inter ? go(rotary_kernel<T, W, true>) : go(rotary_kernel<T, W, false>);
-  else
-    inter ? go(rotary_kernel<T, 1, true>) : go(rotary_kernel<T, 1, false>);
-  return check_launch();
+  auto go = [&](auto kernel) {
+    return launch_dependent(kernel, dim3((unsigned)blocks), kThreads, 0, 1, st, p);
+  };
+  if (wide) return inter ? go(rotary_kernel<T, W, true>) : go(rotary_kernel<T, W, false>);
+  return inter ? go(rotary_kernel<T, 1, true>) : go(rotary_kernel<T, 1, false>);
 }
 
 int validate_plan(const tlsp_rotary_plan* p) {
