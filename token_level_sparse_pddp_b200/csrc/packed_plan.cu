@@ -203,6 +203,20 @@ class Planner {
       if (m == 0) kv0_[s] = 0;
       few_[s] = (int64_t)n * group_ <= kTokenRows;
     }
+    // A few short sequences among longer ones go with their tile items: they end sooner
+    // than those, and save a launch (24 prompts, two of them of 2 and 4 tokens: 244 -> 240 us).
+    if (d_.dtype == TLSP_BF16 && d_.prefix_len == 0) {
+      int64_t longest = 0, most = 0, count = 0;  // keys of a tile item, of a few-query sequence
+      for (int s = 0; s < d_.num_seqs; ++s) {
+        if (!few_[s]) longest = std::max<int64_t>(longest, kv_lens_[s]);
+        if (few_[s] && q_lens_[s] > 0) {
+          most = std::max<int64_t>(most, kv_lens_[s]);
+          ++count;
+        }
+      }
+      if (most <= longest && longest > 0 && count * d_.kv_heads <= kSms / 2)
+        std::fill(few_.begin(), few_.end(), 0);
+    }
     // kernels index tokens with 32 bits (element offsets with 64)
     if (q_rows > 0x7ffffeffLL || kv_rows > 0x7ffffeffLL) return TLSP_ERR_UNSUPPORTED;
     return TLSP_OK;
