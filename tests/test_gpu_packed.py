@@ -1,7 +1,7 @@
 """Packed causal attention with grouped heads and shared-prefix attention on the
 GPU against the definition in 64 bits, within bounds that follow from the
 kernels' arithmetic (tests/packed_ref.py)."""
-import ctypes
+import random
 
 import pytest
 import torch
@@ -386,3 +386,40 @@ def test_rotary_prompt_then_shared_decoding(T):
         O = T.prefix_attention(Q, Kc, Vc, cache_k, cache_v, plan, ws)
         Ref(Q, cache_k, cache_v, [1] * S, [t + 1] * S, starts, True, Kc, Vc).check(O)
         assert ws.status() == T.TLSP_OK
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_batches(T, seed):
+    """Lengths, heads, types, masks, prefixes, cache places and strides drawn at random; a second
+    call returns the same bits."""
+    r = random.Random(seed)
+    d, dtype = r.choice([64, 128]), r.choice([BF16, BF16, BF16, FP32])
+    hk, g = r.choice([1, 2, 3, 8]), r.choice([1, 2, 3, 5, 7, 8, 13, 16])
+    kind = r.choice([[0, 1, 1, 1, 2, 3], [0, 1, 64, 127, 129, 300], [0, 1, 2, 40, 200]])
+    n = r.choice([1, 3, 8, 20])
+    q = [r.choice(kind) for _ in range(n)]
+    kv = [r.choice([a, a + r.randint(0, 1500), r.randint(0, 300), 0]) for a in q]
+    prefix, causal = r.choice([0, 0, 1, 129, 2000]), r.random() < 0.75
+    starts, rows = None, max(1, sum(kv))
+    if r.random() < 0.4:
+        starts, at = [0] * n, r.randint(0, 9)
+        for s in r.sample(range(n), n):
+            starts[s], at = at, at + kv[s] + r.randint(0, 40)
+        rows = max(1, at)
+    Q, K, V, Kp, Vp = inputs(q, kv, hk * g, hk, d, dtype, prefix, seed, rows=sum(q) + 3, kv_rows=rows)
+    if r.random() < 0.3:
+        Q = Q.transpose(0, 1).contiguous().transpose(0, 1)
+    if starts is not None:
+        keep = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        for s in range(n):
+            keep[starts[s]:starts[s] + kv[s]] = True
+        K[~keep], V[~keep] = float("nan"), float("inf")
+    plan = T.PackedPlan(q, kv, hk * g, hk, d, dtype, causal, prefix, starts)
+    ws = plan.workspace()
+    O, lse = attend(T, Q, K, V, Kp, Vp, plan, ws, out=torch.full_like(Q, 9.0))
+    again = attend(T, Q, K, V, Kp, Vp, plan, ws, out=torch.full_like(Q, 9.0))
+    torch.cuda.synchronize()
+    assert ws.status() == T.TLSP_OK
+    assert torch.equal(O, again[0]) and torch.equal(lse, again[1])
+    assert (O[sum(q):] == 9.0).all() and (lse[sum(q):] == 7.0).all()
+    Ref(Q, K, V, q, kv, starts, causal, Kp, Vp).check(O, lse)

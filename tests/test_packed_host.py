@@ -195,6 +195,8 @@ def test_plan_refusals(T):
         assert plan(**bad) == E, bad
     assert plan(h=130, hk=2) == T.TLSP_ERR_UNSUPPORTED          # 65 heads share one
     assert plan(st=(ctypes.c_int64 * 1)(1 << 31)) == T.TLSP_ERR_UNSUPPORTED
+    huge = (ctypes.c_int32 * 1)(0x7ffffe00)                     # too many items, not too few bytes
+    assert plan(h=64, hk=1, q=huge, kv=huge, to=None, size=0) == T.TLSP_ERR_UNSUPPORTED
     assert plan(size=16) == T.TLSP_ERR_WORKSPACE and data.items_bytes > 16
     assert plan(to=None, size=0) == T.TLSP_ERR_WORKSPACE
     assert L.tlsp_packed_make_plan(None, one, one, None, buf, 4096, ctypes.byref(data)) == E
@@ -221,6 +223,7 @@ def test_attention_refusals(T):
                 dict(K=None), dict(V=None), dict(O=None), dict(Q=rows(4, 0)), dict(Q=rows(4, 0x10008)),
                 dict(K=rows(2, rs=0)), dict(K=rows(2, hs=0)), dict(V=rows(2, rs=260)),
                 dict(V=rows(2, hs=132)), dict(O=rows(4, hs=64)), dict(ws=None),
+                dict(O=rows(4, rs=256, hs=128)), dict(O=rows(4, rs=128, hs=384)),
                 dict(ws=ctypes.c_void_p(0x10004)), dict(scale=math.inf), dict(scale=math.nan),
                 dict(lse=ctypes.c_void_p(0x10002)), dict(plan=ctypes.byref(pdata))):
         assert call(**bad) == E, bad

@@ -22,6 +22,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
+constexpr int64_t kMaxItems = int64_t(1) << 22;  // tile items of a plan
 constexpr int kSms = 148;  // planning assumes a B200
 constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
 constexpr int kTokenBlock = 16;        // keys a warp of a token item takes at a time
@@ -219,7 +220,10 @@ class Planner {
     }
     // kernels index tokens with 32 bits (element offsets with 64)
     if (q_rows > 0x7ffffeffLL || kv_rows > 0x7ffffeffLL) return TLSP_ERR_UNSUPPORTED;
-    return TLSP_OK;
+    int64_t items = 0;
+    for (int s = 0; s < d_.num_seqs; ++s)
+      if (!few_[s]) items += ceil_div(q_lens_[s], tile_tokens_);
+    return items > kMaxItems ? TLSP_ERR_UNSUPPORTED : TLSP_OK;
   }
 
   static int32_t clamp_diag(int64_t diag, int64_t kv_n) {
@@ -294,7 +298,7 @@ class Planner {
     const int64_t jobs = (int64_t)loads.size() * d_.kv_heads;
     const int slots = d_.dtype == TLSP_BF16 ? kSms : kSimtCtas * kSms;
     const double mean = total * d_.kv_heads / slots;
-    if (jobs > 16 * slots && longest < mean / 2) return longest;
+    if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return longest;
     const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7, shortest = d_.dtype == TLSP_BF16 ? 4.0 : 1.0;
     double best = longest, least = makespan(loads, d_.kv_heads, longest, fixed, slots);
     auto try_split = [&](double most) {
@@ -519,6 +523,14 @@ int validate_rows(const tlsp_rows* r, int64_t rows, int heads, int d, int size) 
   return TLSP_OK;
 }
 
+// An output's rows and heads must not share memory: one axis steps over the whole other.
+int validate_output(const tlsp_rows* r, int64_t rows, int heads, int d) {
+  if (rows <= 1 || heads <= 1) return TLSP_OK;
+  const bool rows_outside = r->row_stride >= (heads - 1) * r->head_stride + d;
+  const bool heads_outside = r->head_stride >= (rows - 1) * r->row_stride + d;
+  return rows_outside || heads_outside ? TLSP_OK : TLSP_ERR_INVALID_ARG;
+}
+
 // Strides of axes of length 1 are never used: set to something valid.
 tlsp_rows tidy(const tlsp_rows* r, int64_t rows, int heads, int d) {
   tlsp_rows t{};
@@ -548,6 +560,7 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   if (!(std::fabs(scale) < INFINITY)) return TLSP_ERR_INVALID_ARG;
   TLSP_TRY(validate_rows(Q, plan->q_rows, d.heads, d.head_dim, size));
   TLSP_TRY(validate_rows(O, plan->q_rows, d.heads, d.head_dim, size));
+  TLSP_TRY(validate_output(O, plan->q_rows, d.heads, d.head_dim));
   TLSP_TRY(validate_rows(K, plan->kv_rows, d.kv_heads, d.head_dim, size));
   TLSP_TRY(validate_rows(V, plan->kv_rows, d.kv_heads, d.head_dim, size));
   TLSP_TRY(validate_rows(Kp, d.prefix_len, d.kv_heads, d.head_dim, size));

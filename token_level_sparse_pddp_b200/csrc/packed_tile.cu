@@ -217,8 +217,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == kLoadWarp * 32) {
     ptx::prefetch_tmap(&p.tmQ);
-    ptx::prefetch_tmap(&p.tmK);
-    ptx::prefetch_tmap(&p.tmV);
+    if (p.a.kv_rows > 0) {
+      ptx::prefetch_tmap(&p.tmK);
+      ptx::prefetch_tmap(&p.tmV);
+    }
+    if (p.a.prefix_len > 0) {
+      ptx::prefetch_tmap(&p.tmKp);
+      ptx::prefetch_tmap(&p.tmVp);
+    }
   }
   wait_for_previous();
   ptx::tc_fence_before();
