@@ -68,16 +68,17 @@ struct Load {
   }
 };
 
-// Time of tile items on `slots` CTAs taking them longest first when each is cut into
-// parts of at most `most`, and `fixed` is spent on starting and finishing each.
-double makespan(const std::vector<Load>& loads, int kv_heads, double most, double fixed, int slots) {
+// Time of tile items on `slots` CTAs taking them longest first, when item i is cut into
+// parts[i] and `fixed` is spent on starting and finishing each part.
+double makespan(const std::vector<Load>& loads, const std::vector<int64_t>& parts, int kv_heads,
+                double fixed, int slots) {
   std::vector<double> jobs;
-  for (const Load& l : loads) {
-    const int64_t parts = l.parts(most);
-    for (int64_t i = 0; i < parts; ++i)
+  for (size_t x = 0; x < loads.size(); ++x) {
+    const Load& l = loads[x];
+    for (int64_t i = 0; i < parts[x]; ++i)
       for (int h = 0; h < kv_heads; ++h)
-        jobs.push_back((double)(l.steps * (i + 1) / parts - l.steps * i / parts) * l.cost +
-                       fixed * (parts > 1 ? 1.5 : 1));
+        jobs.push_back((double)(l.steps * (i + 1) / parts[x] - l.steps * i / parts[x]) * l.cost +
+                       fixed * (parts[x] > 1 ? 1.5 : 1));
   }
   std::sort(jobs.begin(), jobs.end(), std::greater<double>());
   std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
@@ -136,9 +137,10 @@ class Planner {
         ++i;
       }
     }
-    const double most = tile_split(whole, shared);
-    for (const PackedItem& t : whole) {
-      const int64_t parts = load_of(t).parts(most);
+    const std::vector<int64_t> cut = tile_split(whole, shared);
+    for (size_t x = 0; x < whole.size(); ++x) {
+      const PackedItem& t = whole[x];
+      const int64_t parts = cut[x];
       if (parts == 1) {
         tiles.push_back(t);
         continue;
@@ -148,8 +150,9 @@ class Planner {
       add_merge(t.q0, t.nt, base, parts, t.nt, 0, 0, 0);
     }
     std::vector<Piece> pieces;  // where the prefix results of each token lie
-    for (const PackedItem& t : shared) {
-      const int64_t parts = load_of(t).parts(most), base = take_slots(parts * t.nt);
+    for (size_t x = 0; x < shared.size(); ++x) {
+      const PackedItem& t = shared[x];
+      const int64_t parts = cut[whole.size() + x], base = take_slots(parts * t.nt);
       split(t, parts, base, tiles);
       pieces.push_back({t.q0, t.nt, base, parts});
     }
@@ -280,11 +283,13 @@ class Planner {
     return {steps_of(t), one_tile ? 0.6 : 1.0};
   }
 
-  // Most cost of a tile item. With many more items than SMs they stay whole; else the
-  // split of least estimated time is taken, among those that fill the SMs evenly a few
-  // times over. Starting and finishing an item takes about three steps of 1.7 us (fp32:
-  // 0.7 of 4 us, with three CTAs on an SM).
-  double tile_split(const std::vector<PackedItem>& whole, const std::vector<PackedItem>& shared) {
+  // Parts of each tile item. With many more items than SMs they stay whole; else the
+  // split of least estimated time is taken: all items cut to a size that fills the SMs
+  // evenly a few times over, long items cut to a share of the mean, or only the shortest
+  // ones, those of the last, incomplete round. Starting and finishing an item takes about
+  // three steps of 1.7 us (fp32: 0.7 of 4 us, with three CTAs on an SM).
+  std::vector<int64_t> tile_split(const std::vector<PackedItem>& whole,
+                                  const std::vector<PackedItem>& shared) {
     std::vector<Load> loads;
     double longest = 1, total = 0;
     for (const auto* v : {&whole, &shared})
@@ -294,20 +299,26 @@ class Planner {
         total += all;
         longest = std::max(longest, all);
       }
-    if (loads.empty()) return 1;
+    std::vector<int64_t> best(loads.size(), 1);
+    if (loads.empty()) return best;
     const int64_t jobs = (int64_t)loads.size() * d_.kv_heads;
     const int slots = d_.dtype == TLSP_BF16 ? kSms : kSimtCtas * kSms;
     const double mean = total * d_.kv_heads / slots;
-    if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return longest;
+    if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return best;
     const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7, shortest = d_.dtype == TLSP_BF16 ? 4.0 : 1.0;
-    double best = longest, least = makespan(loads, d_.kv_heads, longest, fixed, slots);
+    double least = makespan(loads, best, d_.kv_heads, fixed, slots);
+    auto try_parts = [&](std::vector<int64_t> parts) {
+      const double t = makespan(loads, parts, d_.kv_heads, fixed, slots);
+      if (t < 0.98 * least) {
+        least = t;
+        best = std::move(parts);
+      }
+    };
     auto try_split = [&](double most) {
       if (most >= longest) return;
-      const double t = makespan(loads, d_.kv_heads, most, fixed, slots);
-      if (t < 0.97 * least) {
-        least = t;
-        best = most;
-      }
+      std::vector<int64_t> parts;
+      for (const Load& l : loads) parts.push_back(l.parts(most));
+      try_parts(std::move(parts));
     };
     for (int rounds = 1; rounds <= 4; ++rounds) {
       if (jobs > (int64_t)rounds * slots) continue;
@@ -320,8 +331,24 @@ class Planner {
       }
       try_split(hi);
     }
-    if (2 * jobs > slots)  // long items among many: cut to a share of the mean
+    if (2 * jobs > slots)
       for (int k = 1; k <= 4; ++k) try_split(std::max(shortest, mean / k));
+    if (jobs > slots && least > 1.03 * (mean + fixed * (double)jobs / slots)) {
+      std::vector<size_t> order(loads.size());
+      for (size_t i = 0; i < order.size(); ++i) order[i] = i;
+      std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) {
+        return (double)loads[a].steps * loads[a].cost > (double)loads[b].steps * loads[b].cost;
+      });
+      for (int64_t rounds = jobs / slots; rounds >= std::max<int64_t>(1, jobs / slots - 1); --rounds)
+        for (int64_t p : {2, 3, 4, 6}) {
+          std::vector<int64_t> parts(loads.size(), 1);
+          for (size_t i = (size_t)(rounds * slots / d_.kv_heads); i < order.size(); ++i) {
+            const Load& l = loads[order[i]];
+            parts[order[i]] = std::max<int64_t>(1, std::min(p, l.steps / 8));
+          }
+          try_parts(std::move(parts));
+        }
+    }
     return best;
   }
 
