@@ -277,6 +277,55 @@ def test_streams_and_captured_replays(T):
             T.PackedPlan([1], [1], 4, 2, 128)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_each_call_reads_the_one_before(T, dtype):
+    """Calls whose queries are the output before them, on one workspace per plan, back to back
+    and as a captured graph: the same bits as with a synchronisation after each call. Tile and
+    token items together, with and without merged parts, either of them alone, and rotary."""
+    heads, kv_heads, d, rows = 8, 2, 128, 424
+    batches = [([1] * 40 + [384], [900 + 37 * i for i in range(40)] + [700], 0),  # both
+               ([1] * 424, [3 * i % 500 for i in range(424)], 900),  # both, merged
+               ([424], [424], 0), ([424], [9000], 0),  # tile items, cut and merged
+               ([4] * 106, [50 + i for i in range(106)], 0),  # token items
+               ([1] * 40 + [384], [500] * 41, 300)]
+    turn = T.RotaryPlan(d)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    steps = []
+    for i, (q, kv, prefix) in enumerate(batches):
+        plan = T.PackedPlan(q, kv, heads, kv_heads, d, dtype, prefix_len=prefix)
+        _, K, V, Kp, Vp = inputs([rows], kv, heads, kv_heads, d, dtype, prefix, seed=i, kv_rows=sum(kv))
+        steps.append((plan, plan.workspace(), K, V, Kp, Vp))
+    first = inputs([rows], [1], heads, kv_heads, d, dtype, seed=9)[0]
+
+    def chain(wait):
+        outs = [torch.empty_like(first) for _ in range(4 * len(steps))]
+        x = first
+        for i, (plan, ws, K, V, Kp, Vp) in enumerate(steps + steps):
+            y, turned = outs[2 * i:2 * i + 2]
+            if Kp is None:
+                T.packed_attention(x, K, V, plan, ws, scale=2.0, out=y)
+            else:
+                T.prefix_attention(x, Kp, Vp, K, V, plan, ws, scale=2.0, out=y)
+            wait()
+            T.rotary(y, None, pos, turn, out=turned)
+            wait()
+            x = turned
+        return outs
+    want = chain(torch.cuda.synchronize)
+    runs = [chain(lambda: None) for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        runs.append(chain(lambda: None))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for outs in runs:
+        for a, b in zip(want, outs):
+            assert torch.equal(a, b)
+    for step in steps:
+        assert step[1].status() == T.TLSP_OK
+
+
 def test_cache_beyond_32_bit_offsets(T):
     """Keys whose element offsets pass 2^32: a cache of 4.3 G elements, of which little is read."""
     kv_rows, hk, d = 4200000, 8, 128

@@ -277,24 +277,40 @@ class Planner {
   }
 
   // A step of an item with one query tile takes 0.6 of one with two (measured with
-  // d = 128: 1.0 us and 1.7 us).
-  Load load_of(const PackedItem& t) const {
+  // d = 128: 1.0 us and 1.7 us), and 0.75 where few-query sequences share the prefix,
+  // whose keys come from memory for a few items only (1.8 and 2.5 us on all SMs).
+  Load load_of(const PackedItem& t, bool shared) const {
     const bool one_tile = d_.dtype == TLSP_BF16 && 2 * t.nt <= tile_tokens_;
-    return {steps_of(t), one_tile ? 0.6 : 1.0};
+    return {steps_of(t), !one_tile ? 1.0 : shared ? 0.75 : 0.6};
+  }
+
+  // Work of the token items in steps of a tile item, with which they share the SMs:
+  // an SM reads about 110 KB of keys and values in the 1.7 us of a step.
+  double token_steps() const {
+    if (d_.dtype != TLSP_BF16) return 0;
+    double keys = 0;
+    for (int s = 0; s < d_.num_seqs; ++s)
+      if (few_[s] && q_lens_[s] > 0) keys += kv_lens_[s];
+    return keys * d_.kv_heads * 4 * d_.head_dim / 110e3;
   }
 
   // Parts of each tile item. With many more items than SMs they stay whole; else the
   // split of least estimated time is taken: all items cut to a size that fills the SMs
   // evenly a few times over, long items cut to a share of the mean, or only the shortest
   // ones, those of the last, incomplete round. Starting and finishing an item takes about
-  // three steps of 1.7 us (fp32: 0.7 of 4 us, with three CTAs on an SM).
+  // three steps of 1.7 us (fp32: 0.7 of 4 us, with three CTAs on an SM). Token items run
+  // on the SMs that tile items leave, so what counts is the sum of both, and fewer and
+  // longer tile items that leave SMs free from the start are tried too: what bounds
+  // these is the matrix rate, what bounds token items the memory (64 sequences of 16 to
+  // 2000 keys behind a prefix of 32760, 40 heads of 128 in 8 groups: one kernel after the
+  // other 106 us, beside each other 98 us with tile items on 144 SMs, 88 us on 104).
   std::vector<int64_t> tile_split(const std::vector<PackedItem>& whole,
                                   const std::vector<PackedItem>& shared) {
     std::vector<Load> loads;
     double longest = 1, total = 0;
     for (const auto* v : {&whole, &shared})
       for (const PackedItem& t : *v) {
-        loads.push_back(load_of(t));
+        loads.push_back(load_of(t, v == &shared));
         const double all = (double)loads.back().steps * loads.back().cost;
         total += all;
         longest = std::max(longest, all);
@@ -306,9 +322,16 @@ class Planner {
     const double mean = total * d_.kv_heads / slots;
     if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return best;
     const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7, shortest = d_.dtype == TLSP_BF16 ? 4.0 : 1.0;
-    double least = makespan(loads, best, d_.kv_heads, fixed, slots);
+    const double beside = token_steps();
+    // estimated time; all SMs busy to the end is the least that a split can give
+    auto time_of = [&](const std::vector<int64_t>& parts) {
+      double sum = total * d_.kv_heads + beside;
+      for (int64_t n : parts) sum += fixed * (n > 1 ? 1.5 : 1) * (double)n * d_.kv_heads;
+      return std::max(makespan(loads, parts, d_.kv_heads, fixed, slots), beside > 0 ? sum / slots : 0);
+    };
+    double least = time_of(best);
     auto try_parts = [&](std::vector<int64_t> parts) {
-      const double t = makespan(loads, parts, d_.kv_heads, fixed, slots);
+      const double t = time_of(parts);
       if (t < 0.98 * least) {
         least = t;
         best = std::move(parts);
@@ -320,17 +343,20 @@ class Planner {
       for (const Load& l : loads) parts.push_back(l.parts(most));
       try_parts(std::move(parts));
     };
-    for (int rounds = 1; rounds <= 4; ++rounds) {
-      if (jobs > (int64_t)rounds * slots) continue;
-      double lo = shortest, hi = longest;  // least cost that gives at most `rounds` items an SM
+    auto try_items = [&](int64_t places) {  // as long as `places` items can be
+      if (jobs > places) return;
+      double lo = shortest, hi = longest;
       for (int i = 0; i < 12; ++i) {
         const double mid = 0.5 * (lo + hi);
         int64_t n = 0;
         for (const Load& l : loads) n += l.parts(mid);
-        (n * d_.kv_heads <= (int64_t)rounds * slots ? hi : lo) = mid;
+        (n * d_.kv_heads <= places ? hi : lo) = mid;
       }
       try_split(hi);
-    }
+    };
+    if (beside > 0)
+      for (int places = slots / 4; places < slots; places += 8) try_items(places);
+    for (int rounds = 1; rounds <= 4; ++rounds) try_items((int64_t)rounds * slots);
     if (2 * jobs > slots)
       for (int k = 1; k <= 4; ++k) try_split(std::max(shortest, mean / k));
     if (jobs > slots && least > 1.03 * (mean + fixed * (double)jobs / slots)) {

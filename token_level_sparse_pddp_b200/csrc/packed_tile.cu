@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   wait_for_previous();
+  let_next_start();  // token items take the SMs that this kernel leaves
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();

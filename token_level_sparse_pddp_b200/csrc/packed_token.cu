@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
-  if (p.after) wait_for_previous();  // what follows this kernel may depend on them
+  // What follows this kernel may depend on the tile items: it ends after them.
+  if (p.after && unit == (int)gridDim.x / cluster - 1) wait_for_previous();
 }
 
 template <int D>
