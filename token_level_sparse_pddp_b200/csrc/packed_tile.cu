@@ -60,7 +60,6 @@ constexpr int kThreads = 640;
 constexpr int kLoadWarp = 16, kQkWarp = 17, kPvWarp = 18, kGuardWarp = 19;
 constexpr int kSlots = 2;  // of K, and of V
 constexpr uint32_t kHalfBytes = kTile * 128;   // 128 rows of 64 channels
-constexpr uint32_t kStageBytes = kTile * 128;  // a query tile's output rows, 128 bytes at a time
 constexpr uint32_t kTmCols = 512;
 constexpr uint32_t kTmP = 128, kTmO = 256;
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -72,8 +71,8 @@ struct Smem {
   static constexpr uint32_t q = 0;
   static constexpr uint32_t k = 2 * tile;
   static constexpr uint32_t v = k + kSlots * tile;
-  static constexpr uint32_t stage = v + kSlots * tile;
-  static constexpr uint32_t bar = stage + 2 * kStageBytes;
+  static constexpr uint32_t sums = v + kSlots * tile;  // fp32 [query tile][half][row]
+  static constexpr uint32_t bar = sums + 4 * kTile * 4;
   static constexpr uint32_t bytes = bar + 512 + 1024;  // + slack to align the base
 };
 
@@ -103,6 +102,7 @@ struct TileParams {
   PackedArgs a;
   CUtensorMap tmQ, tmK, tmV, tmKp, tmVp;
   int tile_tokens;  // of one query tile
+  uint32_t magic;   // row / group = row magic >> 16, rows < 128
   float scale_log2;
 };
 
@@ -170,10 +170,7 @@ __device__ __forceinline__ void set_regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
 }
 
-// kParts: some items write partial results. (With both ways out in one kernel the
-// registers of the chunk loop went to local memory: 24 ragged prompts 270 us
-// instead of 215.)
-template <int D, bool kParts>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_tile_kernel(const __grid_constant__ TileParams p) {
   using S = Smem<D>;
@@ -499,15 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s, half, r, i, gi;  // query tile, keys 64 half .. + 63 of a chunk, row, its token and head
       uint32_t tl;            // TMEM lanes
       __device__ __forceinline__ Place(const TileParams& p, uint32_t tmem) {
-        int t, group;
+        int t;
         asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
-        asm volatile("mov.u32 %0, %1;" : "=r"(group) : "r"(p.a.group));
         s = t >> 8;
         half = (t >> 7) & 1;
         r = t & 127;
-        const int q = r / group;
+        const int q = (int)(r * p.magic >> 16);
         i = q + s * p.tile_tokens;
-        gi = r - q * group;
+        gi = r - q * p.a.group;
         tl = tmem + ((uint32_t)(r & ~31) << 16);
       }
       __device__ __forceinline__ uint32_t o_col() const { return tl + kTmO + s * D + half * kCols; }
@@ -648,120 +644,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars.p_full[s]);
       }
-      // The stage joins the two halves of the row's sum, then takes the rows 128 bytes
-      // at a time: a warp writes pieces of 64 bytes of eight rows.
       const Place at(p, tmem);
-      const uint32_t stage = base + S::stage + at.s * kStageBytes;
-      float* sums = reinterpret_cast<float*>(smem + S::stage + at.s * kStageBytes);
+      float* sums = reinterpret_cast<float*>(smem + S::sums) + at.s * 2 * kTile;
       const bool any = c > c0;
       if (any) {
-        sums[at.half * kTile + at.r] = l_run;
+        sums[at.half * kTile + at.r] = l_run;  // the halves of the row's sum
         wait(&bars.pv_done[s], c - 1);
       }
       if (bar_or(all, 256, *abort_flag != 0)) break;
       const PackedItem it = w.it;
       const bool real = at.real(p, it);
-      const int r = at.r, half = at.half, i = at.i, gi = at.gi;
+      const int half = at.half, i = at.i;
       const uint32_t o_col = at.o_col();
-      const float l = any ? sums[r] + sums[kTile + r] : 0.f;
+      const float l = any ? sums[at.r] + sums[kTile + at.r] : 0.f;
       const bool none = l == 0.f;  // no key seen
       const float inv = none ? 0.f : 1.f / l;
-      const bool part = kParts && it.slot >= 0;
-      const int64_t head0 = (int64_t)w.hk * group;  // first query head of the group
+      const bool part = it.slot >= 0;
+      const int head = w.hk * group + at.gi;
       if (real && half == 0) {
         const float lse = none ? -INFINITY : (m_run + log2f(l)) * kLn2;
         if (part)
-          p.a.part_lse[(int64_t)(it.slot + i) * p.a.heads + head0 + gi] = lse;
+          p.a.part_lse[(int64_t)(it.slot + i) * p.a.heads + head] = lse;
         else if (p.a.lse)
-          p.a.lse[(int64_t)(it.q0 + i) * p.a.heads + head0 + gi] = lse;
+          p.a.lse[(int64_t)(it.q0 + i) * p.a.heads + head] = lse;
       }
       uint32_t any_odd = 0;
       if (any)
         for (int q = 0; q < 8; ++q) any_odd |= bars.odd[k & 1][q];
-      const int rows =  // real rows of the tile
-          (at.s == 0 ? min(it.nt, p.tile_tokens) : max(0, it.nt - p.tile_tokens)) * group;
-      // This thread's pieces of the staged rows: row 32 x + (tid & 255) / 8, piece
-      // tid & 7 (row r's piece g of eight lies in place g ^ (r & 7)).
-      const int g = r & 7, first = (r + 128 * half) >> 3;
-      const uint32_t magic = (65536u + group - 1) / group;  // row / group = row magic >> 16, rows < 128
-      auto write_out = [&](auto put) {
-        uint4 v[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int rr = first + 32 * x;
-          v[x] = ptx::ld_shared_v4(stage + rr * 128 + ((g ^ (rr & 7)) * 16));
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int rr = first + 32 * x, tok = (int)((rr * magic) >> 16);
-          if (rr < rows) put(tok + at.s * p.tile_tokens, rr - tok * group, v[x]);
-        }
-      };
-      if constexpr (!kParts) {  // 32 channels of each half at a time, as bf16
+      // Each thread writes its half of the row from its registers, eight channels at a time:
+      // wider steps, and rows staged in shared memory for stores of whole lines, cost
+      // registers that the chunk loop then lacks (24 ragged prompts 201 us, 16384 tokens
+      // of 12 heads of 64 492 us; 16 channels: 201 and 536 us; staged: 205 and 505 us).
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.O.ptr) +
+                           (int64_t)(it.q0 + i) * p.a.O.row_stride +
+                           (int64_t)head * p.a.O.head_stride + half * kCols;
+      float* part_out =
+          p.a.part_o + ((int64_t)(it.slot + i) * p.a.heads + head) * D + half * kCols;
 #pragma unroll 1
-        for (int q = 0; q < kCols / 32; ++q) {
-          bar_sync(all, 256);  // the sums, or the rows of the last pass, have been read
-#pragma unroll 1
-          for (int b = 0; b < 2; ++b) {
-            uint32_t o[16];
-            if (any) {
-              ptx::tmem_ld16(o_col + q * 32 + b * 16, o);
-              ptx::tmem_ld_wait(o);
-            }
+      for (int q = 0; q < kCols; q += 8) {
+        uint32_t o[8];
+        if (any) ptx::tmem_ld8(o_col + q, o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              o[e] = none ? 0u
-                          : pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              ptx::st_shared_v4(stage + r * 128 + (((half * 4 + b * 2 + e) ^ (r & 7)) * 16), o[4 * e],
-                                o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-          bar_sync(all, 256);
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.O.ptr) +
-                               (int64_t)it.q0 * p.a.O.row_stride + head0 * p.a.O.head_stride +
-                               (g >> 2) * kCols + q * 32 + (g & 3) * 8;
-          write_out([&](int tok, int head, uint4 v) {
-            *reinterpret_cast<uint4*>(out + (int64_t)tok * p.a.O.row_stride +
-                                      head * p.a.O.head_stride) = v;
-          });
-        }
-      } else {  // 16 channels of each half at a time, as fp32
-#pragma unroll 1
-        for (int q = 0; q < kCols / 16; ++q) {
-          uint32_t o[16];
-          if (any) {
-            ptx::tmem_ld16(o_col + q * 16, o);
-            ptx::tmem_ld_wait(o);
-          }
-          bar_sync(all, 256);  // the sums, or the rows of the last pass, have been read
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+        for (int e = 0; e < 8; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+        if (real && part) {
+          uint4* to = reinterpret_cast<uint4*>(part_out + q);
+          to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        } else if (real) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            ptx::st_shared_v4(stage + r * 128 + (((half * 4 + e) ^ (r & 7)) * 16), o[4 * e],
-                              o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          bar_sync(all, 256);
-          const int ch = (g >> 2) * kCols + q * 16 + (g & 3) * 4;
-          write_out([&](int tok, int head, uint4 v) {
-            if (part) {
-              *reinterpret_cast<uint4*>(
-                  p.a.part_o + ((int64_t)(it.slot + tok) * p.a.heads + head0 + head) * D + ch) = v;
-            } else {
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.O.ptr) +
-                                        (int64_t)(it.q0 + tok) * p.a.O.row_stride +
-                                        (head0 + head) * p.a.O.head_stride + ch) =
-                  make_uint2(pack_bf16(__uint_as_float(v.x), __uint_as_float(v.y)),
-                             pack_bf16(__uint_as_float(v.z), __uint_as_float(v.w)));
-            }
-          });
+            o[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          *reinterpret_cast<uint4*>(out + q) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        __syncwarp();
       }
       if (any_odd) {
         // values that are not finite, of keys that only part of the rows see: added to
         // the rows that do, as written
-        bar_sync(all, 256);
 #pragma unroll 1
         for (int q = 0; q < 256 && real; ++q) {
           if (!(bars.odd[k & 1][q >> 5] >> (q & 31) & 1) || q >= i) continue;  // key diag + 1 + q
@@ -769,24 +708,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    (int64_t)(it.kv0 + it.diag + 1 + q) * p.a.V.row_stride +
                                    w.hk * p.a.V.head_stride;
 #pragma unroll 1
-          for (int ch = half * kCols; ch < (half + 1) * kCols; ++ch) {
-            const float z = __bfloat162float(v[ch]);
+          for (int ch = 0; ch < kCols; ++ch) {
+            const float z = __bfloat162float(v[half * kCols + ch]);
             if (fabsf(z) < INFINITY) continue;
-            if (part) {
-              p.a.part_o[((int64_t)(it.slot + i) * p.a.heads + head0 + gi) * D + ch] += z;
-            } else {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.a.O.ptr) +
-                                 (int64_t)(it.q0 + i) * p.a.O.row_stride +
-                                 (head0 + gi) * p.a.O.head_stride + ch;
-              *o = __float2bfloat16_rn(__bfloat162float(*o) + z);
-            }
+            if (part)
+              part_out[ch] += z;
+            else
+              out[ch] = __float2bfloat16_rn(__bfloat162float(out[ch]) + z);
           }
         }
       }
       ptx::tc_fence_before();  // O has been read before the next P is handed over
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bars.work_empty[k & 1]);
-      bar_sync(all, 256);  // the rows of the last pass have been read
     }
   }
 
@@ -812,6 +746,7 @@ int launch(const PackedArgs& a, cudaStream_t st) {
   TileParams p{};
   p.a = a;
   p.tile_tokens = kTcRows / a.group;
+  p.magic = (65536u + a.group - 1) / a.group;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   // Q as (channel, head of the group, key/value head, token)
   const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.group, (uint64_t)a.kv_heads, (uint64_t)a.q_rows};
@@ -823,7 +758,7 @@ int launch(const PackedArgs& a, cudaStream_t st) {
   TLSP_TRY(kv_map(&p.tmV, a.V, a.kv_rows, a.kv_heads, D));
   TLSP_TRY(kv_map(&p.tmKp, a.Kp, a.prefix_len, a.kv_heads, D));
   TLSP_TRY(kv_map(&p.tmVp, a.Vp, a.prefix_len, a.kv_heads, D));
-  auto kernel = a.part_rows > 0 ? packed_tile_kernel<D, true> : packed_tile_kernel<D, false>;
+  auto kernel = packed_tile_kernel<D>;
   TLSP_TRY(ensure_smem_limit((const void*)kernel, (int)Smem<D>::bytes));
   return launch_dependent(kernel, dim3((unsigned)((int64_t)a.n_tiles * a.kv_heads)), kThreads,
                           (int)Smem<D>::bytes, 1, st, p);
