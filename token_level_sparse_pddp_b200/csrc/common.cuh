@@ -47,7 +47,9 @@ int ensure_smem_limit(const void* fn, int bytes);
 // it in the stream is still finishing (programmatic dependent launch): its launch and
 // first instructions then cost no time of their own (1 to 2 us a kernel, back to back).
 // Each block has to execute wait_for_previous() before it touches memory that kernels
-// before may write or read, and before it exits.
+// before may write or read (unless the one before lets it start only after its own wait,
+// and they do not depend on each other), and one block before it exits, so that kernels
+// complete in their order.
 template <class... Params, class... Args>
 int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster,
                      cudaStream_t st, Args... args) {

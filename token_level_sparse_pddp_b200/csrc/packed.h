@@ -94,7 +94,7 @@ __device__ __forceinline__ bool item_ok(const PackedArgs& a, const PackedItem& t
 // packed_tile.cu: tile items on the tensor cores (bf16)
 int packed_tile(const PackedArgs& a, cudaStream_t st);
 // packed_token.cu: token items (bf16)
-// `after`: another kernel of the call precedes it in the stream
+// `after`: behind the tile items of the call, beside which it runs
 int packed_token(const PackedArgs& a, bool after, cudaStream_t st);
 // packed_simt.cu: both kinds of items (fp32)
 int packed_simt(const PackedArgs& a, cudaStream_t st);

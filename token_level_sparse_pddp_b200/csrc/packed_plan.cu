@@ -323,15 +323,25 @@ class Planner {
     if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return best;
     const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7, shortest = d_.dtype == TLSP_BF16 ? 4.0 : 1.0;
     const double beside = token_steps();
-    // estimated time; all SMs busy to the end is the least that a split can give
-    auto time_of = [&](const std::vector<int64_t>& parts) {
-      double sum = total * d_.kv_heads + beside;
-      for (int64_t n : parts) sum += fixed * (n > 1 ? 1.5 : 1) * (double)n * d_.kv_heads;
-      return std::max(makespan(loads, parts, d_.kv_heads, fixed, slots), beside > 0 ? sum / slots : 0);
+    // The least time that a split can take: its longest part's, or all SMs busy to the end.
+    auto bound_of = [&](const std::vector<int64_t>& parts) {
+      double sum = total * d_.kv_heads + beside, most = 0;
+      for (size_t x = 0; x < loads.size(); ++x) {
+        const double each = fixed * (parts[x] > 1 ? 1.5 : 1);
+        sum += each * (double)parts[x] * d_.kv_heads;
+        most = std::max(most, (double)ceil_div(loads[x].steps, parts[x]) * loads[x].cost + each);
+      }
+      return std::max(most, sum / slots);
     };
-    double least = time_of(best);
+    auto time_of = [&](const std::vector<int64_t>& parts, double bound) {
+      const double t = makespan(loads, parts, d_.kv_heads, fixed, slots);
+      return beside > 0 ? std::max(t, bound) : t;
+    };
+    double least = time_of(best, bound_of(best));
     auto try_parts = [&](std::vector<int64_t> parts) {
-      const double t = time_of(parts);
+      const double bound = bound_of(parts);
+      if (bound >= 0.98 * least) return;
+      const double t = time_of(parts, bound);
       if (t < 0.98 * least) {
         least = t;
         best = std::move(parts);
