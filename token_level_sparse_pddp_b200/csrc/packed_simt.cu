@@ -34,7 +34,7 @@ struct Config {
 
 template <int D, int BM, int RM>
 __global__ void __launch_bounds__(Config<D, BM, RM>::threads)
-    packed_simt_kernel(const __grid_constant__ PackedArgs p, const PackedItem* items) {
+    packed_simt_kernel(const __grid_constant__ PackedArgs p, const PackedItem* items, bool after) {
   using C = Config<D, BM, RM>;
   constexpr int DV = D / 16, LD = C::ld, LP = C::lp, kThreads = C::threads;
   extern __shared__ __align__(16) float sm[];
@@ -44,8 +44,11 @@ __global__ void __launch_bounds__(Config<D, BM, RM>::threads)
   float* sP = sV + kBN * LD;
   const PackedItem it = items[blockIdx.x / p.kv_heads];
   const int hk = blockIdx.x % p.kv_heads;
-  wait_for_previous();
-  if (!item_ok(p, it, BM / p.group)) {
+  const bool ok = item_ok(p, it, BM / p.group);
+  // (what the tile items' kernel waited for is done when the token items' starts)
+  if (!after || !ok) wait_for_previous();
+  let_next_start();
+  if (!ok) {
     if (threadIdx.x == 0) record_status(p.status, TLSP_ERR_DEVICE_ASSERT);
     return;
   }
@@ -263,25 +266,27 @@ __global__ void __launch_bounds__(Config<D, BM, RM>::threads)
       *reinterpret_cast<float4*>(o + tx * 4 + c * 16) = y;
     }
   }
+  // What follows this kernel may depend on the tile items: it ends after them.
+  if (after && blockIdx.x == gridDim.x - 1) wait_for_previous();
 }
 
 template <int D, int BM, int RM>
-int launch(const PackedArgs& a, const PackedItem* items, int n, cudaStream_t st) {
+int launch(const PackedArgs& a, const PackedItem* items, int n, bool after, cudaStream_t st) {
   if (n == 0) return TLSP_OK;
   using C = Config<D, BM, RM>;
   auto kernel = packed_simt_kernel<D, BM, RM>;
   TLSP_TRY(ensure_smem_limit((const void*)kernel, C::bytes));
   return launch_dependent(kernel, dim3((unsigned)((int64_t)n * a.kv_heads)), C::threads, C::bytes, 1, st, a,
-                          items);
+                          items, after);
 }
 
 template <int D>
 int run(const PackedArgs& a, cudaStream_t st) {
   if (simt_tile_rows(a.group) == 32)
-    TLSP_TRY((launch<D, 32, 4>(a, a.tiles, a.n_tiles, st)));
+    TLSP_TRY((launch<D, 32, 4>(a, a.tiles, a.n_tiles, false, st)));
   else
-    TLSP_TRY((launch<D, 64, 4>(a, a.tiles, a.n_tiles, st)));
-  return launch<D, kTokenRows, 2>(a, a.tokens, a.n_tokens, st);
+    TLSP_TRY((launch<D, 64, 4>(a, a.tiles, a.n_tiles, false, st)));
+  return launch<D, kTokenRows, 2>(a, a.tokens, a.n_tokens, a.n_tiles > 0, st);
 }
 
 }  // namespace

@@ -441,7 +441,7 @@ def _rotary_tensor(x: torch.Tensor, out: torch.Tensor, rank: int, heads: int) ->
 def _rotary_out(x: torch.Tensor, o: torch.Tensor, dev: int):
     if o.shape != x.shape or o.dtype != x.dtype or o.get_device() != dev:
         raise ValueError("out must match the input's shape, type and device")
-    if any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
+    if 0 in o.stride() and any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
         raise ValueError("out must not be a broadcast tensor")
 
 
