@@ -113,6 +113,15 @@ def test_shared_prefix(T, dtype, d, prefix, q, kv):
         run(T, q, kv, heads, kv_heads, d, dtype, prefix=prefix)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 1), (6, 2), (5, 5)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_short_sequences_share_a_long_prefix(T, d, heads, kv_heads, causal):
+    q = [3, 0, 1, 5, 8, 2, 3, 300, 4, 4, 90, 7, 1]
+    kv = [3, 0, 500, 0, 8, 200, 3, 290, 4, 700, 95, 5, 0]
+    run(T, q, kv, heads, kv_heads, d, BF16, causal, prefix=2100)
+
+
 def test_prefix_without_own_keys(T):
     Q, _, _, Kp, Vp = inputs([1, 40], [0, 0], 4, 2, 128, BF16, prefix=300)
     plan = T.PackedPlan([1, 40], [0, 0], 4, 2, 128, BF16, False, 300)

@@ -170,6 +170,19 @@ def test_plan_covers_random_batches(T):
                     r.randint(0, 1), r.randint(0, 1), r.choice([0, 0, 1, 127, 5000, 30000]))
 
 
+def test_short_sequences_share_a_long_prefix(T):
+    """Sequences of 17 to 64 rows beside others: their rows take the prefix together."""
+    r = random.Random(8)
+    for _ in range(40):
+        heads, kv_heads = r.choice([(8, 1), (6, 2), (12, 12), (40, 8), (17, 1), (64, 1)])
+        q = [r.choice([0, 1, 2, 3, 5, 9, r.randint(1, 90)]) for _ in range(r.randint(1, 24))]
+        kv = [r.choice([0, n, n + r.randint(0, 400), r.randint(0, 9)]) for n in q]
+        check_cover(T, q, kv, heads, kv_heads, 128, 1, r.randint(0, 1), r.choice([2047, 2048, 9000]))
+    q = [3] * 16                                        # 24 rows each, three in a query tile
+    _, tiles, _, _ = make(T, q, [40] * 16, heads=8, kv_heads=1, prefix=15329)
+    assert sum(-(-int(t[5]) // 128) for t in tiles) < 2 * 120 + 30  # two items' steps, cut
+
+
 def test_long_caches_are_split(T):
     """A single token behind a long cache is shared out over many CTAs."""
     data, tiles, tokens, merges = make(T, [1], [60000], heads=12, kv_heads=4)

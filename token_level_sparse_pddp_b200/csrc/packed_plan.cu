@@ -23,8 +23,10 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
 constexpr int64_t kMaxItems = int64_t(1) << 22;  // tile items of a plan
+constexpr int kSharedKeys = 2048;  // of a prefix whose work is shared by longer sequences too
 constexpr int kSms = 148;  // planning assumes a B200
 constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
+constexpr int kGpcs = 8;               // a cluster's CTAs lie in one of them
 constexpr int kTokenBlock = 16;        // keys a warp of a token item takes at a time
 constexpr int kSimtCtas = 3;  // fp32 tile items that share an SM
 constexpr int kChunk = 128;  // keys a tile item takes at a time
@@ -108,18 +110,26 @@ class Planner {
     TLSP_TRY(place());
     // Tile items first; those left whole, then those split.
     std::vector<PackedItem> whole;
+    std::vector<int> own;  // sequences whose prefix part is shared: their items of own keys
     for (int s = 0; s < d_.num_seqs; ++s)
-      if (!few_[s])
+      if (!share_[s])
         for (int t0 = 0; t0 < q_lens_[s]; t0 += tile_tokens_) whole.push_back(own_tile(s, t0));
-    std::vector<PackedItem> shared;  // rows of few-query sequences against the prefix
+    const size_t owns = whole.size();  // those items stand from here
+    for (int s = 0; s < d_.num_seqs; ++s)
+      if (share_[s] && !few_[s]) {
+        own.push_back(s);
+        whole.push_back(own_tile(s, 0));
+        whole.back().pre_n = 0;
+      }
+    std::vector<PackedItem> shared;  // rows of short sequences against the prefix
     if (d_.prefix_len > 0) {
       for (int s = 0; s < d_.num_seqs;) {
-        if (!few_[s]) {
+        if (!share_[s]) {
           ++s;
           continue;
         }
         int e = s;  // a run of such sequences: their queries are consecutive
-        while (e < d_.num_seqs && few_[e]) ++e;
+        while (e < d_.num_seqs && share_[e]) ++e;
         const int64_t q0 = q0_[s], n = q0_[e - 1] + q_lens_[e - 1] - q0;
         for (int64_t i = 0; i < n; i += tile_tokens_)
           shared.push_back({(int32_t)(q0 + i), (int32_t)std::min<int64_t>(tile_tokens_, n - i), 0, 0, 0,
@@ -138,16 +148,20 @@ class Planner {
       }
     }
     const std::vector<int64_t> cut = tile_split(whole, shared);
+    std::vector<Piece> own_parts;
     for (size_t x = 0; x < whole.size(); ++x) {
       const PackedItem& t = whole[x];
-      const int64_t parts = cut[x];
-      if (parts == 1) {
+      const int64_t parts = x >= owns && t.kv_n == 0 ? 0 : cut[x];
+      if (x < owns && parts == 1) {
         tiles.push_back(t);
         continue;
       }
       const int64_t base = take_slots(parts * t.nt);
-      split(t, parts, base, tiles);
-      add_merge(t.q0, t.nt, base, parts, t.nt, 0, 0, 0);
+      if (parts > 0) split(t, parts, base, tiles);
+      if (x < owns)
+        add_merge(t.q0, t.nt, base, parts, t.nt, 0, 0, 0);
+      else
+        own_parts.push_back({t.q0, t.nt, base, parts});
     }
     std::vector<Piece> pieces;  // where the prefix results of each token lie
     for (size_t x = 0; x < shared.size(); ++x) {
@@ -160,6 +174,9 @@ class Planner {
       plan_tokens(shared_tokens, pieces);
     else
       plan_tokens_simt(shared_tokens, pieces);
+    size_t at = 0;  // (the pieces ascend)
+    for (size_t x = 0; x < own.size(); ++x)
+      merge_sequence(own[x], own_parts[x].slot, own_parts[x].parts, pieces, at);
     if (part_rows_ > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
     // longest first: the grid is handed out in this order
     auto longer = [](const PackedItem& a, const PackedItem& b) {
@@ -220,6 +237,20 @@ class Planner {
       }
       if (most <= longest && longest > 0 && count * d_.kv_heads <= kSms / 2)
         std::fill(few_.begin(), few_.end(), 0);
+    }
+    // Sequences that fill at most half of a query tile share the work on a long prefix too
+    // (their own keys are items of their own, merged with it), if one beside them does: 48
+    // sequences of 1 to 3 tokens behind 15329 keys, 16 / 2 heads: 31 us, with the prefix
+    // alone for each of 3 tokens (24 rows) 62 us.
+    share_ = few_;
+    if (d_.dtype == TLSP_BF16 && d_.prefix_len >= kSharedKeys) {
+      auto may = [&](int s) { return few_[s] || 4 * (int64_t)q_lens_[s] <= tile_tokens_; };
+      for (int s = 0; s < d_.num_seqs;) {
+        int e = s, n = 0;
+        for (; e < d_.num_seqs && may(e); ++e) n += q_lens_[e] > 0;
+        if (n > 1) std::fill(share_.begin() + s, share_.begin() + e, 1);
+        s = std::max(e, s + 1);
+      }
     }
     // kernels index tokens with 32 bits (element offsets with 64)
     if (q_rows > 0x7ffffeffLL || kv_rows > 0x7ffffeffLL) return TLSP_ERR_UNSUPPORTED;
@@ -321,7 +352,10 @@ class Planner {
     const int slots = d_.dtype == TLSP_BF16 ? kSms : kSimtCtas * kSms;
     const double mean = total * d_.kv_heads / slots;
     if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return best;
-    const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7, shortest = d_.dtype == TLSP_BF16 ? 4.0 : 1.0;
+    const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7;
+    // No part is shorter, which bounds the merging (bf16, few tokens before long caches on
+    // an empty GPU: 13 to 17 us, with 4 instead 17 to 21, with 1 no better).
+    const double shortest = d_.dtype == TLSP_BF16 ? 2.0 : 1.0;
     const double beside = token_steps();
     // The least time that a split can take: its longest part's, or all SMs busy to the end.
     auto bound_of = [&](const std::vector<int64_t>& parts) {
@@ -507,15 +541,21 @@ class Planner {
       total += d.keys;
     }
     const int64_t jobs = (int64_t)drafts.size() * d_.kv_heads;
-    while (cluster < kMaxCluster && jobs * 2 * cluster <= kTokenSlots && longest > 64 * cluster)
+    // Places beside the tile items, if they are enough (else most start behind those: all).
+    // A wider cluster than they take would wait for the end of tile items: 8 sequences of
+    // 1 to 30 tokens 20 us instead of 16.
+    int64_t places = kTokenSlots - 2 * (int64_t)tiles.size() * d_.kv_heads;
+    if (places < jobs || places < kGpcs) places = kTokenSlots;
+    const int64_t widest = std::min<int64_t>(kMaxCluster, places / kGpcs);  // that fits into what is free
+    while (2 * cluster <= widest && jobs * 2 * cluster <= places && longest > 64 * cluster)
       cluster *= 2;
     // Items of more keys than a cluster's share are cut: where the GPU would stay empty,
     // to fill it; else at twice the mean keys of a place for a CTA, 512 at least.
-    const int64_t mean = ceil_div(total * d_.kv_heads, kTokenSlots);
+    const int64_t mean = ceil_div(total * d_.kv_heads, places);
     int64_t range = std::max<int64_t>(512, 2 * mean) * cluster;
-    if (jobs * cluster * 2 <= kTokenSlots) {
+    if (jobs * cluster * 2 <= places) {
       range = 256 * cluster;
-      while (parts_of(lens, range) * d_.kv_heads * cluster > kTokenSlots) range += 32 * cluster;
+      while (parts_of(lens, range) * d_.kv_heads * cluster > places) range += 32 * cluster;
     }
     for (Draft& d : drafts) {
       d.parts = d.seq >= 0 && d.keys == 0 ? 0 : std::max<int64_t>(1, ceil_div(d.keys, range));
@@ -570,7 +610,8 @@ class Planner {
   const int64_t* kv_starts_;
   int group_, tile_tokens_;
   std::vector<int64_t> q0_, kv0_;
-  std::vector<char> few_;
+  std::vector<char> few_;    // sequences of at most kTokenRows rows
+  std::vector<char> share_;  // those, and others that share the work on the prefix
   int64_t part_rows_ = 0;
 };
 
