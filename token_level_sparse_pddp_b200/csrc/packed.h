@@ -69,6 +69,7 @@ struct PackedArgs {
   const TokenSegment* segments;
   const MergeItem* merges;
   int n_tiles, n_tokens, n_segments, n_merges;
+  int merge_parts;  // most parts of a merge item
   int cluster;  // CTAs of a token item (bf16)
   int heads, kv_heads, group, d;
   int64_t q_rows, kv_rows, prefix_len, part_rows;

@@ -1,7 +1,8 @@
 // Joins the partial results of rows whose keys were split over several items:
 //   O = sum_p e^(lse_p - lse) O_p with lse = log sum_p e^(lse_p).
 //
-// One warp per row. 64 tokens x 40 heads of 128, 6 to 7 parts each: 6.8 us alone. Bound by latency (a few dependent reads of L2), so it starts
+// One warp per row, or, with many parts, a block (128 tokens of 2 heads behind a prefix in
+// 118 parts, tile items and merge: 29 us with a warp, 24 with a block). Bound by latency (a few dependent reads of L2), so it starts
 // while the kernel before is finishing, reads its item meanwhile, and then has
 // eight parts' rows in flight with their log partitions. fp32 throughout; parts are
 // added in their order, so results do not depend on which CTA was first.
@@ -11,7 +12,7 @@ namespace tlsp {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kAhead = 8;  // parts in flight
+constexpr int kAhead = 8;  // parts in flight for a warp
 
 template <int D>
 struct Row;  // a lane's channels of a row
@@ -49,12 +50,13 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[E]) {
     *reinterpret_cast<__nv_bfloat162*>(p + e) = __floats2bfloat162_rn(x[e], x[e + 1]);
 }
 
-template <class T, int D>
+// kJoint: the block's warps share a row's parts, else each takes a row.
+template <class T, int D, bool kJoint>
 __global__ void __launch_bounds__(32 * kWarps)
     packed_merge_kernel(const __grid_constant__ PackedArgs p) {
   const MergeItem it = p.merges[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kWarps + warp;
+  const int row = kJoint ? blockIdx.y : blockIdx.y * kWarps + warp;
   const int i = row / p.heads, h = row % p.heads;
   const int parts = it.a_parts + it.b_parts;
   const bool ok = it.q0 >= 0 && it.nt >= 1 && (int64_t)it.q0 + it.nt <= p.q_rows &&
@@ -79,8 +81,10 @@ __global__ void __launch_bounds__(32 * kWarps)
   constexpr int E = D / 32;
   float acc[E] = {};
   float m = -INFINITY, sum = 0.f;  // running maximum of the log partitions
-  for (int q0 = 0; q0 < parts; q0 += 32) {  // 32 parts: a lane each for the weights
-    const int n = min(32, parts - q0);
+  const int first = kJoint ? (int)((int64_t)parts * warp / kWarps) : 0;
+  const int last = kJoint ? (int)((int64_t)parts * (warp + 1) / kWarps) : parts;
+  for (int q0 = first; q0 < last; q0 += 32) {  // 32 parts: a lane each for the weights
+    const int n = min(32, last - q0);
     const float lse = lane < n ? p.part_lse[part_row(q0 + lane)] : -INFINITY;
     Row<D> rows[kAhead];
 #pragma unroll
@@ -104,6 +108,28 @@ __global__ void __launch_bounds__(32 * kWarps)
         }
     }
   }
+  if constexpr (kJoint) {
+    __shared__ float s_acc[kWarps][D], s_m[kWarps], s_sum[kWarps];
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_sum[warp] = sum;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w]);
+    const float use = m == -INFINITY ? 0.f : m;
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = expf(s_m[w] - use);
+      sum = fmaf(f, s_sum[w], sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, s_acc[w][lane * E + e], acc[e]);
+    }
+  }
   const bool none = sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
 #pragma unroll
@@ -115,10 +141,14 @@ __global__ void __launch_bounds__(32 * kWarps)
 
 template <class T>
 int merge(const PackedArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)a.n_merges, (unsigned)ceil_div((int64_t)kMergeTokens * a.heads, kWarps));
+  // More parts than a warp has in flight: the block's warps share them.
+  const bool joint = a.merge_parts > kAhead;
+  const dim3 grid((unsigned)a.n_merges,
+                  (unsigned)ceil_div((int64_t)kMergeTokens * a.heads, joint ? 1 : kWarps));
   if (grid.y > 65535) return TLSP_ERR_UNSUPPORTED;
-  return launch_dependent(a.d == 128 ? packed_merge_kernel<T, 128> : packed_merge_kernel<T, 64>, grid,
-                          32 * kWarps, 0, 1, st, a);
+  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * kWarps, 0, 1, st, a); };
+  if (joint) return a.d == 128 ? go(packed_merge_kernel<T, 128, true>) : go(packed_merge_kernel<T, 64, true>);
+  return a.d == 128 ? go(packed_merge_kernel<T, 128, false>) : go(packed_merge_kernel<T, 64, false>);
 }
 
 }  // namespace

@@ -23,7 +23,6 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
 constexpr int64_t kMaxItems = int64_t(1) << 22;  // tile items of a plan
-constexpr int kSharedKeys = 2048;  // of a prefix whose work is shared by longer sequences too
 constexpr int kSms = 148;  // planning assumes a B200
 constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
 constexpr int kGpcs = 8;               // a cluster's CTAs lie in one of them
@@ -147,7 +146,7 @@ class Planner {
         ++i;
       }
     }
-    const std::vector<int64_t> cut = tile_split(whole, shared);
+    const std::vector<int64_t> cut = tile_split(whole, shared, shared_tokens);
     std::vector<Piece> own_parts;
     for (size_t x = 0; x < whole.size(); ++x) {
       const PackedItem& t = whole[x];
@@ -238,26 +237,60 @@ class Planner {
       if (most <= longest && longest > 0 && count * d_.kv_heads <= kSms / 2)
         std::fill(few_.begin(), few_.end(), 0);
     }
-    // Sequences that fill at most half of a query tile share the work on a long prefix too
-    // (their own keys are items of their own, merged with it), if one beside them does: 48
-    // sequences of 1 to 3 tokens behind 15329 keys, 16 / 2 heads: 31 us, with the prefix
-    // alone for each of 3 tokens (24 rows) 62 us.
-    share_ = few_;
-    if (d_.dtype == TLSP_BF16 && d_.prefix_len >= kSharedKeys) {
-      auto may = [&](int s) { return few_[s] || 4 * (int64_t)q_lens_[s] <= tile_tokens_; };
-      for (int s = 0; s < d_.num_seqs;) {
-        int e = s, n = 0;
-        for (; e < d_.num_seqs && may(e); ++e) n += q_lens_[e] > 0;
-        if (n > 1) std::fill(share_.begin() + s, share_.begin() + e, 1);
-        s = std::max(e, s + 1);
-      }
-    }
+    choose_shared();
     // kernels index tokens with 32 bits (element offsets with 64)
     if (q_rows > 0x7ffffeffLL || kv_rows > 0x7ffffeffLL) return TLSP_ERR_UNSUPPORTED;
     int64_t items = 0;
     for (int s = 0; s < d_.num_seqs; ++s)
       if (!few_[s]) items += ceil_div(q_lens_[s], tile_tokens_);
     return items > kMaxItems ? TLSP_ERR_UNSUPPORTED : TLSP_OK;
+  }
+
+  // Short sequences share the work on the prefix: their rows take it together, and their
+  // own keys are items of their own, merged with it. Those of a token item always do; longer
+  // ones, of up to a tile item, where that is less work (in steps of a tile item): 48
+  // sequences of 1 to 3 tokens behind 15329 keys, 16 / 2 heads: 31 us, with the prefix alone
+  // for each of 3 tokens (24 rows) 62 us.
+  void choose_shared() {
+    share_ = few_;
+    if (d_.dtype != TLSP_BF16 || d_.prefix_len == 0) return;
+    const double pre = (double)ceil_div(d_.prefix_len, kChunk);
+    const int64_t half = tile_tokens_ / 2;
+    auto own_steps = [&](int s) { return (double)ceil_div(own_tile(s, 0).kv_n, kChunk); };
+    // sequences of up to `most` tokens share, if one beside them does: work of all that might
+    auto work = [&](int64_t most, std::vector<char>& share) {
+      double sum = 0;
+      for (int s = 0; s < d_.num_seqs;) {
+        int e = s, n = 0;
+        int64_t tokens = 0;
+        for (; e < d_.num_seqs && (few_[e] || q_lens_[e] <= most); ++e) {
+          n += q_lens_[e] > 0;
+          tokens += q_lens_[e];
+        }
+        const int end = std::max(e, s + 1);
+        if (e > s && (n > 1 || few_[s])) {
+          const int64_t rest = tokens % tile_tokens_;
+          sum += pre * ((double)(tokens / tile_tokens_) +
+                        (rest == 0 ? 0 : rest * group_ <= kTokenRows ? 0.5 : rest <= half ? 0.75 : 1.0));
+        }
+        for (; s < end; ++s) {
+          share[(size_t)s] = few_[s] || (e > s && n > 1);
+          if (few_[s] || q_lens_[s] > tile_tokens_) continue;  // the same either way
+          const double steps = own_steps(s) + (share[(size_t)s] ? 0.0 : pre);
+          sum += 3 + steps * (q_lens_[s] <= half ? 0.6 : 1.0);
+        }
+      }
+      return sum;
+    };
+    double least = work(0, share_);
+    for (int64_t most : {half / 2, half, (int64_t)tile_tokens_}) {
+      std::vector<char> share = few_;
+      const double w = work(most, share);
+      if (w < 0.9 * least) {
+        least = w;
+        share_ = std::move(share);
+      }
+    }
   }
 
   static int32_t clamp_diag(int64_t diag, int64_t kv_n) {
@@ -315,14 +348,17 @@ class Planner {
     return {steps_of(t), !one_tile ? 1.0 : shared ? 0.75 : 0.6};
   }
 
+  double keys_of_step() const { return 110e3 / (4 * d_.head_dim); }
+
   // Work of the token items in steps of a tile item, with which they share the SMs:
   // an SM reads about 110 KB of keys and values in the 1.7 us of a step.
-  double token_steps() const {
+  double token_steps(const std::vector<PackedItem>& shared_tokens) const {
     if (d_.dtype != TLSP_BF16) return 0;
     double keys = 0;
+    for (const PackedItem& t : shared_tokens) keys += t.pre_n;
     for (int s = 0; s < d_.num_seqs; ++s)
       if (few_[s] && q_lens_[s] > 0) keys += kv_lens_[s];
-    return keys * d_.kv_heads * 4 * d_.head_dim / 110e3;
+    return keys * d_.kv_heads / keys_of_step();
   }
 
   // Parts of each tile item. With many more items than SMs they stay whole; else the
@@ -336,7 +372,8 @@ class Planner {
   // 2000 keys behind a prefix of 32760, 40 heads of 128 in 8 groups: one kernel after the
   // other 106 us, beside each other 98 us with tile items on 144 SMs, 88 us on 104).
   std::vector<int64_t> tile_split(const std::vector<PackedItem>& whole,
-                                  const std::vector<PackedItem>& shared) {
+                                  const std::vector<PackedItem>& shared,
+                                  const std::vector<PackedItem>& shared_tokens) {
     std::vector<Load> loads;
     double longest = 1, total = 0;
     for (const auto* v : {&whole, &shared})
@@ -351,12 +388,13 @@ class Planner {
     const int64_t jobs = (int64_t)loads.size() * d_.kv_heads;
     const int slots = d_.dtype == TLSP_BF16 ? kSms : kSimtCtas * kSms;
     const double mean = total * d_.kv_heads / slots;
+    tile_time_ = mean;
     if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return best;
     const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7;
     // No part is shorter, which bounds the merging (bf16, few tokens before long caches on
     // an empty GPU: 13 to 17 us, with 4 instead 17 to 21, with 1 no better).
     const double shortest = d_.dtype == TLSP_BF16 ? 2.0 : 1.0;
-    const double beside = token_steps();
+    const double beside = token_steps(shared_tokens);
     // The least time that a split can take: its longest part's, or all SMs busy to the end.
     auto bound_of = [&](const std::vector<int64_t>& parts) {
       double sum = total * d_.kv_heads + beside, most = 0;
@@ -419,6 +457,7 @@ class Planner {
           try_parts(std::move(parts));
         }
     }
+    tile_time_ = least;
     return best;
   }
 
@@ -541,11 +580,14 @@ class Planner {
       total += d.keys;
     }
     const int64_t jobs = (int64_t)drafts.size() * d_.kv_heads;
-    // Places beside the tile items, if they are enough (else most start behind those: all).
+    // Places beside the tile items, if they are enough and done with their share before
+    // those are (else most start behind those: all).
     // A wider cluster than they take would wait for the end of tile items: 8 sequences of
     // 1 to 30 tokens 20 us instead of 16.
     int64_t places = kTokenSlots - 2 * (int64_t)tiles.size() * d_.kv_heads;
-    if (places < jobs || places < kGpcs) places = kTokenSlots;
+    if (places < std::max<int64_t>(jobs, kGpcs) ||
+        (double)total * d_.kv_heads / (double)places > tile_time_ * keys_of_step() / 2)
+      places = kTokenSlots;
     const int64_t widest = std::min<int64_t>(kMaxCluster, places / kGpcs);  // that fits into what is free
     while (2 * cluster <= widest && jobs * 2 * cluster <= places && longest > 64 * cluster)
       cluster *= 2;
@@ -613,6 +655,7 @@ class Planner {
   std::vector<char> few_;    // sequences of at most kTokenRows rows
   std::vector<char> share_;  // those, and others that share the work on the prefix
   int64_t part_rows_ = 0;
+  double tile_time_ = 0;  // of the tile items, in steps
 };
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -685,6 +728,7 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   a.n_tiles = plan->tile_items;
   a.n_tokens = plan->token_items;
   a.n_merges = plan->merge_items;
+  a.merge_parts = plan->merge_parts;
   a.heads = d.heads;
   a.kv_heads = d.kv_heads;
   a.group = d.heads / d.kv_heads;
@@ -737,6 +781,8 @@ int tlsp_packed_make_plan(const tlsp_packed_desc* desc, const int32_t* q_lens,
     out.token_items = (int32_t)(p.tokens.size() + p.token_items.size());
     out.token_segments = (int32_t)p.segments.size();
     out.cluster = p.cluster;
+    for (const MergeItem& t : p.merges)
+      out.merge_parts = std::max(out.merge_parts, t.a_parts + t.b_parts);
     out.merge_items = (int32_t)p.merges.size();
     out.q_rows = p.q_rows;
     out.kv_rows = p.kv_rows;

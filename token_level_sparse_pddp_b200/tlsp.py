@@ -79,7 +79,7 @@ class PackedPlanData(ctypes.Structure):
     _fields_ = [("desc", PackedDesc), ("tile_items", ctypes.c_int32),
                 ("token_items", ctypes.c_int32), ("token_segments", ctypes.c_int32),
                 ("merge_items", ctypes.c_int32), ("cluster", ctypes.c_int32),
-                ("reserved", ctypes.c_int32), ("q_rows", ctypes.c_int64),
+                ("merge_parts", ctypes.c_int32), ("q_rows", ctypes.c_int64),
                 ("kv_rows", ctypes.c_int64), ("part_rows", ctypes.c_int64),
                 ("items_bytes", ctypes.c_uint64), ("ws_bytes", ctypes.c_uint64)]
 
