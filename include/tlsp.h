@@ -340,7 +340,7 @@ typedef struct {
   tlsp_packed_desc desc;
   int32_t tile_items, token_items, token_segments, merge_items;
   int32_t cluster;     /* CTAs that share a token item */
-  int32_t merge_parts;    /* most partial rows of a token */
+  int32_t merge_parts; /* most partial rows of a token */
   int64_t q_rows;      /* query tokens of all sequences */
   int64_t kv_rows;     /* rows K and V must have (the furthest key + 1) */
   int64_t part_rows;   /* query tokens x key ranges whose partial results are merged */
