@@ -27,7 +27,6 @@ constexpr int kSms = 148;  // planning assumes a B200
 constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
 constexpr int kGpcs = 8;               // a cluster's CTAs lie in one of them
 constexpr int kTokenBlock = 16;        // keys a warp of a token item takes at a time
-constexpr int kSimtCtas = 3;  // fp32 tile items that share an SM
 constexpr int kChunk = 128;  // keys a tile item takes at a time
 
 int validate_desc(const tlsp_packed_desc* d) {
@@ -348,6 +347,10 @@ class Planner {
     return {steps_of(t), !one_tile ? 1.0 : shared ? 0.75 : 0.6};
   }
 
+  // fp32 tile items that share an SM: as many as its registers and shared memory take (with
+  // 3 for 4 and for 2 here, six ragged sequences with d = 64 took 72 us instead of 65.5, and
+  // with d = 128 85 us instead of 73).
+  int simt_ctas() const { return (d_.head_dim == 64 ? 4 : 2) / (group_ > 32 ? 2 : 1); }
   double keys_of_step() const { return 110e3 / (4 * d_.head_dim); }
 
   // Work of the token items in steps of a tile item, with which they share the SMs:
@@ -365,7 +368,7 @@ class Planner {
   // split of least estimated time is taken: all items cut to a size that fills the SMs
   // evenly a few times over, long items cut to a share of the mean, or only the shortest
   // ones, those of the last, incomplete round. Starting and finishing an item takes about
-  // three steps of 1.7 us (fp32: 0.7 of 4 us, with three CTAs on an SM). Token items run
+  // three steps of 1.7 us (fp32: 0.7 of a step). Token items run
   // on the SMs that tile items leave, so what counts is the sum of both, and fewer and
   // longer tile items that leave SMs free from the start are tried too: what bounds
   // these is the matrix rate, what bounds token items the memory (64 sequences of 16 to
@@ -386,7 +389,7 @@ class Planner {
     std::vector<int64_t> best(loads.size(), 1);
     if (loads.empty()) return best;
     const int64_t jobs = (int64_t)loads.size() * d_.kv_heads;
-    const int slots = d_.dtype == TLSP_BF16 ? kSms : kSimtCtas * kSms;
+    const int slots = d_.dtype == TLSP_BF16 ? kSms : simt_ctas() * kSms;
     const double mean = total * d_.kv_heads / slots;
     tile_time_ = mean;
     if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return best;
