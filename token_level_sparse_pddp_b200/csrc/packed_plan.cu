@@ -27,7 +27,6 @@ constexpr int kSms = 148;  // planning assumes a B200
 constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
 constexpr int kGpcs = 8;               // a cluster's CTAs lie in one of them
 constexpr int kTokenBlock = 16;        // keys a warp of a token item takes at a time
-constexpr int kChunk = 128;  // keys a tile item takes at a time
 
 int validate_desc(const tlsp_packed_desc* d) {
   if (!d) return TLSP_ERR_INVALID_ARG;
@@ -51,11 +50,6 @@ WsLayout ws_layout(const tlsp_packed_plan& p) {
   L.o = align_up(L.lse + sizeof(float) * (size_t)p.part_rows * p.desc.heads);
   L.total = align_up(L.o + sizeof(float) * (size_t)p.part_rows * p.desc.heads * p.desc.head_dim);
   return L;
-}
-
-// Chunks of 128 keys a tile item steps through.
-int64_t steps_of(const PackedItem& t) {
-  return ceil_div(t.pre_n, kChunk) + ceil_div(t.kv_n, kChunk);
 }
 
 // An item's steps, and what one of them costs.
@@ -101,6 +95,7 @@ class Planner {
           const int64_t* kv_starts)
       : d_(d), q_lens_(q_lens), kv_lens_(kv_lens), kv_starts_(kv_starts) {
     group_ = d.heads / d.kv_heads;
+    chunk_ = d.dtype == TLSP_BF16 ? 128 : 64;
     tile_tokens_ = tile_tokens(d.dtype == TLSP_BF16, group_);
   }
 
@@ -177,7 +172,7 @@ class Planner {
       merge_sequence(own[x], own_parts[x].slot, own_parts[x].parts, pieces, at);
     if (part_rows_ > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
     // longest first: the grid is handed out in this order
-    auto longer = [](const PackedItem& a, const PackedItem& b) {
+    auto longer = [&](const PackedItem& a, const PackedItem& b) {
       return steps_of(a) > steps_of(b);
     };
     std::stable_sort(tiles.begin(), tiles.end(), longer);
@@ -253,9 +248,9 @@ class Planner {
   void choose_shared() {
     share_ = few_;
     if (d_.dtype != TLSP_BF16 || d_.prefix_len == 0) return;
-    const double pre = (double)ceil_div(d_.prefix_len, kChunk);
+    const double pre = (double)ceil_div(d_.prefix_len, chunk_);
     const int64_t half = tile_tokens_ / 2;
-    auto own_steps = [&](int s) { return (double)ceil_div(own_tile(s, 0).kv_n, kChunk); };
+    auto own_steps = [&](int s) { return (double)ceil_div(own_tile(s, 0).kv_n, chunk_); };
     // sequences of up to `most` tokens share, if one beside them does: work of all that might
     auto work = [&](int64_t most, std::vector<char>& share) {
       double sum = 0;
@@ -292,6 +287,9 @@ class Planner {
     }
   }
 
+  // Chunks of keys a tile item steps through.
+  int64_t steps_of(const PackedItem& t) const { return ceil_div(t.pre_n, chunk_) + ceil_div(t.kv_n, chunk_); }
+
   static int32_t clamp_diag(int64_t diag, int64_t kv_n) {
     return (int32_t)std::max<int64_t>(-0x40000000LL, std::min<int64_t>(diag, kv_n));
   }
@@ -308,15 +306,15 @@ class Planner {
 
   // Cuts an item's keys (prefix, then own) at whole chunks into `parts`.
   void split(const PackedItem& t, int64_t parts, int64_t base, std::vector<PackedItem>& to) {
-    const int64_t pre_steps = ceil_div(t.pre_n, kChunk), steps = steps_of(t);
+    const int64_t pre_steps = ceil_div(t.pre_n, chunk_), steps = steps_of(t);
     for (int64_t p = 0; p < parts; ++p) {
       const int64_t a = steps * p / parts, b = steps * (p + 1) / parts;
       PackedItem x = t;
-      const int64_t pa = std::min(a, pre_steps) * kChunk, pb = std::min(b, pre_steps) * kChunk;
+      const int64_t pa = std::min(a, pre_steps) * chunk_, pb = std::min(b, pre_steps) * chunk_;
       x.pre0 = (int32_t)(t.pre0 + std::min<int64_t>(pa, t.pre_n));
       x.pre_n = (int32_t)(std::min<int64_t>(pb, t.pre_n) - std::min<int64_t>(pa, t.pre_n));
-      const int64_t oa = std::max<int64_t>(0, a - pre_steps) * kChunk;
-      const int64_t ob = std::max<int64_t>(0, b - pre_steps) * kChunk;
+      const int64_t oa = std::max<int64_t>(0, a - pre_steps) * chunk_;
+      const int64_t ob = std::max<int64_t>(0, b - pre_steps) * chunk_;
       x.kv0 = (int32_t)(t.kv0 + std::min<int64_t>(oa, t.kv_n));
       x.kv_n = (int32_t)(std::min<int64_t>(ob, t.kv_n) - std::min<int64_t>(oa, t.kv_n));
       x.diag = clamp_diag((int64_t)t.diag - oa, x.kv_n);
@@ -368,7 +366,7 @@ class Planner {
   // split of least estimated time is taken: all items cut to a size that fills the SMs
   // evenly a few times over, long items cut to a share of the mean, or only the shortest
   // ones, those of the last, incomplete round. Starting and finishing an item takes about
-  // three steps of 1.7 us (fp32: 0.7 of a step). Token items run
+  // three steps of 1.7 us (fp32: one). Token items run
   // on the SMs that tile items leave, so what counts is the sum of both, and fewer and
   // longer tile items that leave SMs free from the start are tried too: what bounds
   // these is the matrix rate, what bounds token items the memory (64 sequences of 16 to
@@ -393,7 +391,7 @@ class Planner {
     const double mean = total * d_.kv_heads / slots;
     tile_time_ = mean;
     if (jobs > 16 * slots && (longest < mean / 2 || jobs > 100000)) return best;
-    const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 0.7;
+    const double fixed = d_.dtype == TLSP_BF16 ? 3.0 : 1.0;
     // No part is shorter, which bounds the merging (bf16, few tokens before long caches on
     // an empty GPU: 13 to 17 us, with 4 instead 17 to 21, with 1 no better).
     const double shortest = d_.dtype == TLSP_BF16 ? 2.0 : 1.0;
@@ -471,8 +469,8 @@ class Planner {
     for (int s = 0; s < d_.num_seqs; ++s)
       if (few_[s] && q_lens_[s] > 0 && kv_lens_[s] > 0) lens.push_back(kv_lens_[s]);
     for (const PackedItem& t : shared_tokens) lens.push_back(t.pre_n);
-    int64_t range = kChunk;
-    while (range < 2048 && parts_of(lens, range) * d_.kv_heads > kTokenSlots) range += kChunk;
+    int64_t range = chunk_;
+    while (range < 2048 && parts_of(lens, range) * d_.kv_heads > kTokenSlots) range += chunk_;
     return range;
   }
 
@@ -654,6 +652,7 @@ class Planner {
   const int32_t *q_lens_, *kv_lens_;
   const int64_t* kv_starts_;
   int group_, tile_tokens_;
+  int chunk_;  // keys a tile item takes at a time
   std::vector<int64_t> q0_, kv0_;
   std::vector<char> few_;    // sequences of at most kTokenRows rows
   std::vector<char> share_;  // those, and others that share the work on the prefix
