@@ -359,8 +359,9 @@ def test_refusals(T):
     Q, K, V, Kp, Vp = inputs(q, kv, 4, 2, 128, BF16, 5)
     plan, pplan = T.PackedPlan(q, kv, 4, 2, 128), T.PackedPlan(q, kv, 4, 2, 128, prefix_len=5)
     ws, small = pplan.workspace(), T.Workspace.status_only()
-    many = inputs([1] * 40, [9] * 40, 4, 2, 128, BF16, 5)       # shared tiles: partial results
-    mplan = T.PackedPlan([1] * 40, [9] * 40, 4, 2, 128, prefix_len=5)
+    many = inputs([300], [20000], 4, 2, 128, BF16)               # cut keys: partial results
+    mplan = T.PackedPlan([300], [20000], 4, 2, 128)
+    assert mplan.data.part_rows > 0
     before = T.launch_count()
     bad = [
         lambda: T.packed_attention(Q[:3], K, V, plan, ws),
@@ -387,8 +388,7 @@ def test_refusals(T):
             f()
             pytest.fail(f"call {i} was not refused")
     status = [
-        (T.TLSP_ERR_WORKSPACE, lambda: T.prefix_attention(many[0], many[3], many[4], many[1], many[2],
-                                                          mplan, small)),
+        (T.TLSP_ERR_WORKSPACE, lambda: T.packed_attention(*many[:3], mplan, small)),
         (T.TLSP_ERR_INVALID_ARG, lambda: T.packed_attention(Q, K[:, :1].expand(12, 2, 128), V, plan, ws)),
         (T.TLSP_ERR_INVALID_ARG, lambda: T.PackedPlan([-1], [1], 4, 2, 128)),
         (T.TLSP_ERR_INVALID_ARG, lambda: T.PackedPlan([1], [1], 4, 3, 128)),

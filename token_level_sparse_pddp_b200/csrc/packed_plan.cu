@@ -26,6 +26,7 @@ constexpr int64_t kMaxItems = int64_t(1) << 22;  // tile items of a plan
 constexpr int kSms = 148;  // planning assumes a B200
 constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
 constexpr int kGpcs = 8;               // a cluster's CTAs lie in one of them
+constexpr int kTokenKeys = 107;        // that such a CTA takes in 1.7 us
 constexpr int kTokenBlock = 16;        // keys a warp of a token item takes at a time
 
 int validate_desc(const tlsp_packed_desc* d) {
@@ -124,6 +125,16 @@ class Planner {
         int e = s;  // a run of such sequences: their queries are consecutive
         while (e < d_.num_seqs && share_[e]) ++e;
         const int64_t q0 = q0_[s], n = q0_[e - 1] + q_lens_[e - 1] - q0;
+        if (as_token_items(s, e)) {
+          for (int x = s; x < e;) {
+            const int y = end_of_group(x, e);
+            const int64_t nt = q0_[y - 1] + q_lens_[y - 1] - q0_[x];
+            if (nt > 0) shared.push_back({(int32_t)q0_[x], (int32_t)nt, 0, 0, 0, d_.prefix_len, 0, 0});
+            x = y;
+          }
+          s = e;
+          continue;
+        }
         for (int64_t i = 0; i < n; i += tile_tokens_)
           shared.push_back({(int32_t)(q0 + i), (int32_t)std::min<int64_t>(tile_tokens_, n - i), 0, 0, 0,
                             d_.prefix_len, 0, 0});
@@ -285,6 +296,43 @@ class Planner {
         share_ = std::move(share);
       }
     }
+  }
+
+  // The sequences from x on, before e, whose rows fit into a token item together.
+  int end_of_group(int x, int e) const {
+    int64_t tokens = 0;
+    int y = x;
+    for (; y < e && (tokens + q_lens_[y]) * group_ <= kTokenRows; ++y) tokens += q_lens_[y];
+    return y;
+  }
+  // Whether a run of few-query sequences takes the prefix in token items of up to 16 rows,
+  // with their own keys and nothing to merge, not in tile items: the prefix is read for
+  // every 16 rows then, but tile items and merge take some 4 steps besides their work (21
+  // sequences of one token behind 334 keys, 3 / 1 heads: 10 us instead of 13.5).
+  bool as_token_items(int s, int e) const {
+    if (d_.dtype != TLSP_BF16) return false;
+    int64_t keys = 0, longest = 0, tokens = 0, jobs = 0;
+    for (int x = s; x < e;) {
+      if (!few_[x]) return false;
+      const int y = end_of_group(x, e);
+      int64_t all = 0;
+      for (int i = x; i < y; ++i)
+        if (q_lens_[i] > 0) {
+          all += kv_lens_[i];
+          tokens += q_lens_[i];
+        }
+      if (q0_[y - 1] + q_lens_[y - 1] > q0_[x]) all += d_.prefix_len;
+      keys += all;
+      longest = std::max(longest, all);
+      jobs += all > 0 ? d_.kv_heads : 0;
+      x = y;
+    }
+    int ctas = 1;  // of an item
+    while (ctas < kMaxCluster && jobs * 2 * ctas <= kTokenSlots) ctas *= 2;
+    const double each = std::max((double)keys * d_.kv_heads / kTokenSlots, (double)longest / ctas);
+    const double tile_work = (double)ceil_div(d_.prefix_len, chunk_) *
+                             (double)ceil_div(tokens, tile_tokens_) * d_.kv_heads / kSms;
+    return each / kTokenKeys <= 4 + tile_work;
   }
 
   // Chunks of keys a tile item steps through.
