@@ -10,7 +10,7 @@
 // filled by 16-byte cp.async while the other is used: V(j) comes in under Q K(j)^T,
 // K(j + 1) under P V(j).
 // Measured, six ragged sequences (1850 tokens, 2989 keys, 8 / 2 heads, d = 64):
-// 69 us = 21 TFLOP/s, of which 8 us to merge; 8 x 1024 queries and keys without mask 35 TFLOP/s (packed FMAs
+// 65.5 us = 23 TFLOP/s, with the merge; 8 x 1024 queries and keys without mask 35 TFLOP/s (packed FMAs
 // alone reach 64 in a loop on registers; shared-memory wavefronts are 74% busy, the
 // FMA pipe 57%; 64-row items and 8 rows per thread measured within 3% of this).
 // A masked key has weight 0, and 0 x inf is NaN: rows behind the key range are stored
