@@ -15,9 +15,9 @@
 // all of them. It loads the pieces of a batch of heads before it writes the first: in
 // and out may be the same memory, so the compiler cannot do that by itself. The heads
 // are split over threads only as far as filling the GPU needs.
-// Measured (12 + 12 heads x 32760 tokens x 128, bf16, 403 MB): 69.7 us = 5.8 TB/s with
+// Measured (12 + 12 heads x 32760 tokens x 128, bf16, 403 MB): 69 us = 5.8 TB/s with
 // batches of two heads, 74 with four (fewer threads fit), 90 without batches. fp32
-// (2 x 24 heads x 4680 x 64, 115 MB): 18.7 us = 6.1 TB/s with four, 20.2 with two:
+// (2 x 24 heads x 4680 x 64, 115 MB): 19 us = 6.0 TB/s with four, 20.2 with two:
 // 16 bytes hold half as many pairs, so angles and registers weigh half as much.
 #include <cmath>
 
@@ -46,16 +46,39 @@ template <class T>
 constexpr int kBatch = sizeof(T) == 2 ? 2 : 4;  // heads loaded at once
 constexpr int kThreads = 128;
 
-// cos and sin (times the amplitude) of pair i at position index (b, n)
-__device__ __forceinline__ void turn_of(const RotaryParams& p, int i, int b, int n, float& c,
-                                        float& s) {
-  const int64_t at = p.plan.axis[i] * p.pos_axis + b * p.pos_batch + n;
-  const int64_t pos = p.pos64 ? reinterpret_cast<const int64_t*>(p.pos)[at]
-                              : (int64_t) reinterpret_cast<const int32_t*>(p.pos)[at];
-  const uint64_t turn = (uint64_t)pos * p.plan.turns[i];
-  sincospif((float)(int32_t)(turn >> 32) * (1.f / 2147483648.f), &s, &c);
-  c *= p.plan.amplitude;
-  s *= p.plan.amplitude * p.sign;
+// The plan lies among the kernel's parameters, from where lanes that read different
+// entries get them one after the other. Through an address whose origin the compiler does
+// not see they come like global memory (37762 tokens of 3 + 1 heads of 128: 25 us, 38 us
+// the other way).
+template <class E>
+__device__ __forceinline__ const E* as_memory(const E* p) {
+  asm volatile("" : "+l"(p));
+  return p;
+}
+
+// cos and sin (times the amplitude) of pairs i .. i + V - 1 (the first `count` are used) at
+// position index (b, n)
+template <int V>
+__device__ __forceinline__ void turns_of(const RotaryParams& p, int i, int count, int b, int n,
+                                         float (&c)[V], float (&s)[V]) {
+  const uint64_t* turns = as_memory(p.plan.turns) + i;
+  const uint8_t* axis = as_memory(p.plan.axis) + i;
+  const int64_t at = b * p.pos_batch + n;
+  auto position = [&](int64_t x) {
+    return p.pos64 ? reinterpret_cast<const int64_t*>(p.pos)[x]
+                   : (int64_t) reinterpret_cast<const int32_t*>(p.pos)[x];
+  };
+  const bool one = p.plan.axes == 1;
+  const int64_t first = one ? position(at) : 0;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if (e >= count) break;
+    const int64_t pos = one ? first : position(axis[e] * p.pos_axis + at);
+    const uint64_t turn = (uint64_t)pos * turns[e];
+    sincospif((float)(int32_t)(turn >> 32) * (1.f / 2147483648.f), &s[e], &c[e]);
+    c[e] *= p.plan.amplitude;
+    s[e] *= p.plan.amplitude * p.sign;
+  }
 }
 
 template <class T>
@@ -122,8 +145,10 @@ __device__ __forceinline__ void turn(float& x1, float& x2, float c, float s) {
 // two pieces of V channels at c0 and c1 (the second may be missing): with the half
 // layout channel c0 + e pairs with c1 + e, with the interleaved one neighbours within
 // a piece do (V = 1: c0 with c1 in both). Units behind rot_units copy.
+// (bf16: 64 registers, for the threads that hide the reads; fp32 spills with that: 21.2 us
+// instead of 19.7.)
 template <class T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 1) rotary_kernel(const __grid_constant__ RotaryParams p) {
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int u = (int)(id % p.units);
   const int64_t rest = id / p.units;
@@ -150,9 +175,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       c0 = kInter ? 2 * u : u * V;
       c1 = kInter ? c0 + 1 : R / 2 + c0;
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (two || e < V / 2) turn_of(p, u * V + e, b, n, c[e], s[e]);
+    turns_of<V>(p, u * V, two ? V : V / 2, b, n, c, s);
   } else {
     c0 = R + 2 * (u - p.rot_units) * V;
     c1 = c0 + V;
@@ -224,10 +247,11 @@ int launch(RotaryParams& p, const tlsp_rotary_call& call, bool two, cudaStream_t
   p.batches[0] = (int)ceil_div(p.t[0].heads, kBatch<T>);
   p.batches[1] = two ? (int)ceil_div(p.t[1].heads, kBatch<T>) : 0;
   const int64_t rows = (int64_t)p.batch * p.tokens;
-  // Enough threads to fill the GPU (bf16: twice over, 69.7 us for the case above
-  // against 72 with a quarter; fp32: half, 18.7 us against 23), but no more than that:
-  // each further split computes the angles once more.
-  const int64_t want = (int64_t)device_sm_count() * (sizeof(T) == 2 ? 4096 : 1024);
+  // Enough threads to fill the GPU, but no more than that: each further split computes the
+  // angles once more (bf16, 37762 tokens of 3 + 1 heads: 15 us, 25 with 4096 threads an SM;
+  // the case above 69 us with 1536, 76 with 8192. fp32, the case above: 19.7 us with 1024,
+  // 20.7 with 768, 23.8 with 2048).
+  const int64_t want = (int64_t)device_sm_count() * (sizeof(T) == 2 ? 1536 : 1024);
   const int64_t split = std::min<int64_t>(p.batches[0] + p.batches[1],
                                           std::max<int64_t>(1, ceil_div(want, rows * p.units)));
   p.head_split = (int)split;
