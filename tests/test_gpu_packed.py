@@ -335,6 +335,33 @@ def test_each_call_reads_the_one_before(T, dtype):
         assert step[1].status() == T.TLSP_OK
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("q,kv,prefix", [
+    ([1] * 8, [900 + 37 * i for i in range(8)], 0),                # token items alone
+    ([1] * 2, [20000, 17], 0),                                     # cut and merged
+    ([300], [9000], 0),                                            # tile items, cut and merged
+    ([1] * 40 + [384], [500] * 40 + [700], 900),                   # both, merged
+])
+def test_tables_written_just_before(T, dtype, q, kv, prefix):
+    """A plan's table that kernels ahead in the stream write (in turn all zeros, which no kernel
+    takes for items, and the table) is read as stream order has it."""
+    tensors = inputs(q, kv, 8, 2, 128, dtype, prefix)
+    plan = T.PackedPlan(q, kv, 8, 2, 128, dtype, prefix_len=prefix)
+    ws, table = plan.workspace(), plan.items.clone()
+    want = attend(T, *tensors, plan, ws)
+    zero = torch.zeros_like(table)
+    outs = []
+    for _ in range(10):
+        torch.add(zero, 0, out=plan.items)
+        torch.add(table, 0, out=plan.items)
+        outs.append(attend(T, *tensors, plan, ws))
+        outs.append(attend(T, *tensors, plan, ws))
+    torch.cuda.synchronize()
+    assert ws.status() == T.TLSP_OK
+    for O, lse in outs:
+        assert torch.equal(O, want[0]) and torch.equal(lse, want[1])
+
+
 def test_cache_beyond_32_bit_offsets(T):
     """Keys whose element offsets pass 2^32: a cache of 4.3 G elements, of which little is read."""
     kv_rows, hk, d = 4200000, 8, 128

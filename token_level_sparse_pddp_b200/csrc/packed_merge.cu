@@ -4,10 +4,11 @@
 // One warp per row, or, with many parts, a block (128 tokens of 2 heads behind a prefix in
 // 118 parts, tile items and merge: 29 us with a warp, 24 with a block). Bound by latency
 // (a few dependent reads of L2; 64 tokens x 40 heads of 128, 6 to 7 parts each: 6.8 us
-// alone), so it starts while the kernel before is finishing, reads its item meanwhile, and
-// then has eight parts' rows in flight for a warp with their log partitions. fp32
-// throughout; parts are added in a fixed order, so results do not depend on which CTA was
-// first.
+// alone), so it starts while the kernel before is finishing, reads its item meanwhile (the
+// other kernels of a call let the next one start only when what came before the call is
+// done, so the table is there), and then has eight parts' rows in flight for a warp with
+// their log partitions. fp32 throughout; parts are added in a fixed order, so results do
+// not depend on which CTA was first.
 #include "packed.h"
 
 namespace tlsp {

@@ -42,13 +42,14 @@ __global__ void __launch_bounds__(Config<D, BM, RM>::threads)
   float* sK = sQ + BM * LD;
   float* sV = sK + kBN * LD;
   float* sP = sV + kBN * LD;
+  // Before anything is read, the table included: kernels before may write it. (What the
+  // tile items' kernel waited for is done when the token items' starts.)
+  if (!after) wait_for_previous();
+  let_next_start();
   const PackedItem it = items[blockIdx.x / p.kv_heads];
   const int hk = blockIdx.x % p.kv_heads;
-  const bool ok = item_ok(p, it, BM / p.group);
-  // (what the tile items' kernel waited for is done when the token items' starts)
-  if (!after || !ok) wait_for_previous();
-  let_next_start();
-  if (!ok) {
+  if (!item_ok(p, it, BM / p.group)) {
+    if (after) wait_for_previous();
     if (threadIdx.x == 0) record_status(p.status, TLSP_ERR_DEVICE_ASSERT);
     return;
   }

@@ -110,10 +110,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cluster = p.a.cluster, unit = blockIdx.x / cluster;
   const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
   const int hk = unit % p.a.kv_heads;
-  const TokenItem it = p.a.token_items[unit / p.a.kv_heads];
   const int group = p.a.group;
   for (int e = threadIdx.x; e < 16 * D / 16; e += kThreads)
     reinterpret_cast<uint4*>(s_odd)[e] = make_uint4(0, 0, 0, 0);
+  // Before anything is read, the tables included: kernels before may write them. (What the
+  // tile items' kernel waited for is done when this one starts behind it.)
+  if (!p.after) wait_for_previous();
+  let_next_start();
+  const TokenItem it = p.a.token_items[unit / p.a.kv_heads];
   // Lane l holds segment l; its first block is the blocks before it.
   TokenSegment sg{};
   bool ok = it.nt >= 1 && it.nt <= kTokenRows / group && it.q0 >= 0 &&
@@ -127,10 +131,8 @@ __global__ void __launch_bounds__(kThreads, 2)
          sg.diag >= -0x40000000 && sg.diag <= sg.n;
   }
   ok = __all_sync(0xffffffffu, ok);  // the same for every warp of the cluster
-  let_next_start();
-  // (what the tile items' kernel waited for is done when this one starts behind it)
-  if (!p.after || !ok) wait_for_previous();
   if (!ok) {
+    if (p.after) wait_for_previous();
     if (threadIdx.x == 0) record_status(p.a.status, TLSP_ERR_DEVICE_ASSERT);
     return;
   }
