@@ -335,6 +335,27 @@ def test_each_call_reads_the_one_before(T, dtype):
         assert step[1].status() == T.TLSP_OK
 
 
+def test_a_dropped_workspace_of_another_stream(T):
+    """Dropped while a call on the plan's stream still waits to run, a workspace that another
+    stream made is not handed out there again."""
+    q, kv = [1] * 2, [20000, 17]
+    Q, K, V, _, _ = inputs(q, kv, 6, 2, 128, BF16)
+    plan, other = T.PackedPlan(q, kv, 6, 2, 128), torch.cuda.Stream()
+    assert plan.data.part_rows > 0
+    with torch.cuda.stream(other):
+        ws = plan.workspace()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)               # about 0.1 s of the current stream
+    O = T.packed_attention(Q, K, V, plan, ws)
+    at, nbytes = ws.buf.data_ptr(), ws.nbytes
+    del ws
+    with torch.cuda.stream(other):
+        again = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    assert not torch.cuda.current_stream().query() and again.data_ptr() != at
+    torch.cuda.synchronize()
+    Ref(Q, K, V, q, kv).check(O)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("q,kv,prefix", [
     ([1] * 8, [900 + 37 * i for i in range(8)], 0),                # token items alone

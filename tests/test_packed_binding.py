@@ -1,0 +1,77 @@
+"""The binding of the packed attention and rotary calls without a GPU: what it checks and keeps
+before it calls the library."""
+import types
+
+import pytest
+import torch
+
+from token_level_sparse_pddp_b200 import build as tlsp_build
+
+
+@pytest.fixture(scope="module")
+def T():
+    tlsp_build.build()
+    from token_level_sparse_pddp_b200 import tlsp
+    tlsp.lib()
+    return tlsp
+
+
+@pytest.fixture
+def calls(T, monkeypatch):
+    """Library calls of the binding, recorded in place of being made; a current stream that a
+    test sets (`calls.stream`), on "device" -1, where CPU tensors lie."""
+    made = types.SimpleNamespace(stream=5, list=[])
+
+    def launch(device, fn, *args):
+        made.list.append(fn.__name__)
+        return T.TLSP_OK
+    monkeypatch.setattr(T, "_launch", launch)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: made.stream, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda dev=None: types.SimpleNamespace(cuda_stream=made.stream))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return made
+
+
+class Buffer:
+    """Stands for a device buffer: notes the streams it is recorded on."""
+
+    def __init__(self):
+        self.recorded = []
+
+    def get_device(self):
+        return -1
+
+    def data_ptr(self):
+        return 4096
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+def plan_of(T, q, kv, heads=4, kv_heads=2, d=64, made_on=5, prefix=0):
+    return types.SimpleNamespace(q_rows=sum(q), kv_rows=sum(kv), heads=heads, kv_heads=kv_heads,
+                                 head_dim=d, dtype=torch.float32, prefix_len=prefix, device="cpu",
+                                 items=Buffer(), _at=0, _dev=-1, _made_on=made_on)
+
+
+def workspace(T, made_on):
+    ws = object.__new__(T.Workspace)
+    ws.nbytes, ws.buf, ws.made_on = 1 << 20, Buffer(), made_on
+    return ws
+
+
+def tensors(q, kv, heads=4, kv_heads=2, d=64):
+    return torch.zeros(q, heads, d), torch.zeros(kv, kv_heads, d), torch.zeros(kv, kv_heads, d)
+
+
+@pytest.mark.parametrize("plan_on,ws_on,now,plan_kept,ws_kept", [
+    (5, 5, 5, [], []), (5, 6, 5, [], [5]), (6, 5, 5, [5], []), (6, 7, 5, [5], [5]),
+])
+def test_memory_of_other_streams_is_kept(T, calls, plan_on, ws_on, now, plan_kept, ws_kept):
+    """Plan and workspace are each recorded on the calling stream if they were made on another."""
+    plan, ws = plan_of(T, [3], [3], made_on=plan_on), workspace(T, ws_on)
+    calls.stream = now
+    T.packed_attention(*tensors(3, 3), plan, ws)
+    assert calls.list == ["tlsp_packed_attention"]
+    assert plan.items.recorded == plan_kept and ws.buf.recorded == ws_kept

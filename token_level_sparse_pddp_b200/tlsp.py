@@ -198,6 +198,7 @@ class Workspace:
             raise TlspError(TLSP_ERR_INVALID_ARG, "tlsp_workspace_bytes")
         self.nbytes = n
         self.buf = torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+        self.made_on = torch.cuda.current_stream(self.buf.device).cuda_stream
 
     @classmethod
     def status_only(cls, device=None) -> "Workspace":
@@ -624,12 +625,15 @@ def _packed(Q, Kp, Vp, K, V, plan: PackedPlan, ws: Workspace, scale, out, lse):
         scale = 0.0
     elif scale == 0.0:
         raise ValueError("scale must not be 0")
-    if torch._C._cuda_getCurrentRawStream(dev) != plan._made_on and \
+    here = torch._C._cuda_getCurrentRawStream(dev)
+    if (here != plan._made_on or here != ws.made_on) and \
             not torch.cuda.is_current_stream_capturing():
-        # their memory is not reused before this call is done
+        # what was made on another stream is not reused before this call is done
         stream = torch.cuda.current_stream(dev)
-        plan.items.record_stream(stream)
-        ws.buf.record_stream(stream)
+        if here != plan._made_on:
+            plan.items.record_stream(stream)
+        if here != ws.made_on:
+            ws.buf.record_stream(stream)
     items, at = plan.items.data_ptr(), plan._at
     if plan.prefix_len:
         kp = _packed_rows(Kp, "K_prefix", plan.prefix_len, hk, plan)
