@@ -209,6 +209,16 @@ def test_sequences_that_share_an_item(T, d):
     assert torch.isnan(ref.O).any() and torch.isinf(ref.O).any()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens,heads", [(1, 1), (1, 3), (1, 5), (3, 5), (1, 7), (1, 11), (1, 15)])
+def test_odd_rows_of_a_cluster(T, d, tokens, heads):
+    """Items of an odd number of rows shared by the CTAs of a cluster: with d = 64 half of a warp
+    has an element less to join than the other half."""
+    plan = T.PackedPlan([tokens] * 2, [1200, 700], heads, 1, d)
+    assert plan.data.cluster > 1 and plan.data.tile_items == 0
+    run(T, [tokens] * 2, [1200, 700], heads, 1, d)
+
+
 def test_rows_behind_the_last_sequence(T):
     q, kv = [40, 1], [40, 300]
     Q, K, V, _, _ = inputs(q, kv, 4, 2, 128, BF16, rows=60, kv_rows=400)
