@@ -153,7 +153,8 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
          ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
 
-// Barrier of `threads` threads; true if `vote` was, in any of them.
+// Barrier of `threads` threads; true if `vote` was, in any of them. (These barriers count
+// threads; what follows them here, TMEM accesses, asks for converged warps.)
 __device__ __forceinline__ bool bar_or(int id, int threads, bool vote) {
   uint32_t any;
   asm volatile(
@@ -162,10 +163,12 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool vote) {
       : "=r"(any)
       : "r"((uint32_t)vote), "r"(id), "r"(threads)
       : "memory");
+  __syncwarp();
   return any != 0;
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+  __syncwarp();
 }
 
 // 640 threads start with 96 registers each; the 512 of the softmax need a few more
@@ -687,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            (int64_t)head * p.a.O.head_stride + half * kCols;
       float* part_out =
           p.a.part_o + ((int64_t)(it.slot + i) * p.a.heads + head) * D + half * kCols;
+      __syncwarp();
 #pragma unroll 1
       for (int q = 0; q < kCols; q += 8) {
         uint32_t o[8];
