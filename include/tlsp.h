@@ -354,7 +354,9 @@ typedef struct {
  * NULL); plan->items_bytes is what is needed.
  *   q_lens, kv_lens   [num_seqs], each >= 0, on the host.
  *   kv_starts         [num_seqs] first key row of each sequence (for caches
- *                     with room behind each sequence), or NULL: end to end. */
+ *                     with room behind each sequence), or NULL: end to end.
+ * TLSP_ERR_UNSUPPORTED: more than 2^31 - 257 query, key or prefix rows, or more work
+ * items than a grid holds. */
 int tlsp_packed_make_plan(const tlsp_packed_desc* desc, const int32_t* q_lens,
                           const int32_t* kv_lens, const int64_t* kv_starts, void* items,
                           size_t items_bytes, tlsp_packed_plan* plan);

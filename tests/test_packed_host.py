@@ -333,3 +333,23 @@ def test_rotary_refusals(T):
     broken.axis[3] = 1
     assert call(plan=broken) == E
     assert L.tlsp_launch_count() == before
+
+
+# ------------------------------------------------------------------ values out of range
+
+@pytest.mark.parametrize("start", [2 ** 63 - 1, 2 ** 63 - 2, 2 ** 62, 0x7ffffeff - 24])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_starts_whose_end_is_out_of_range(T, start, dtype):
+    """Sequences that would end behind the largest key row, sums that do not fit included."""
+    data = T.PackedPlanData()
+    desc = T.PackedDesc(1, 4, 2, 128, dtype, 1, 0)
+    buf = (ctypes.c_char * 65536)()
+    q, kv = (ctypes.c_int32 * 1)(20), (ctypes.c_int32 * 1)(25)
+
+    def plan(start):
+        return T.lib().tlsp_packed_make_plan(ctypes.byref(desc), q, kv, (ctypes.c_int64 * 1)(start),
+                                             buf, len(buf), ctypes.byref(data))
+    assert plan(start) == T.TLSP_ERR_UNSUPPORTED
+    assert plan(0x7ffffeff - 25) == T.TLSP_OK and data.kv_rows == 0x7ffffeff
+    desc.prefix_len = 0x7fffff00
+    assert plan(0) == T.TLSP_ERR_UNSUPPORTED

@@ -23,6 +23,7 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
 constexpr int64_t kMaxItems = int64_t(1) << 22;  // tile items of a plan
+constexpr int64_t kMaxRows = 0x7ffffeff;  // kernels index tokens with 32 bits (element offsets with 64)
 constexpr int kSms = 148;  // planning assumes a B200
 constexpr int kTokenSlots = 2 * kSms;  // CTAs of token items resident at once
 constexpr int kGpcs = 8;               // a cluster's CTAs lie in one of them
@@ -216,12 +217,14 @@ class Planner {
     kv0_.resize(d_.num_seqs);
     few_.resize(d_.num_seqs);
     int64_t end = 0;
+    if (d_.prefix_len > kMaxRows) return TLSP_ERR_UNSUPPORTED;
     for (int s = 0; s < d_.num_seqs; ++s) {
       const int32_t n = q_lens_[s], m = kv_lens_[s];
       if (n < 0 || m < 0) return TLSP_ERR_INVALID_ARG;
       q0_[s] = q_rows;
       kv0_[s] = kv_starts_ ? kv_starts_[s] : end;
       if (kv0_[s] < 0) return TLSP_ERR_INVALID_ARG;
+      if (m > 0 && kv0_[s] > kMaxRows - m) return TLSP_ERR_UNSUPPORTED;
       end += m;
       q_rows += n;
       if (m > 0) kv_rows = std::max(kv_rows, kv0_[s] + m);
@@ -243,8 +246,7 @@ class Planner {
         std::fill(few_.begin(), few_.end(), 0);
     }
     choose_shared();
-    // kernels index tokens with 32 bits (element offsets with 64)
-    if (q_rows > 0x7ffffeffLL || kv_rows > 0x7ffffeffLL) return TLSP_ERR_UNSUPPORTED;
+    if (q_rows > kMaxRows) return TLSP_ERR_UNSUPPORTED;
     int64_t items = 0;
     for (int s = 0; s < d_.num_seqs; ++s)
       if (!few_[s]) items += ceil_div(q_lens_[s], tile_tokens_);
@@ -742,7 +744,7 @@ int validate_packed(const tlsp_packed_plan* p) {
   if (!p) return TLSP_ERR_INVALID_ARG;
   TLSP_TRY(validate_desc(&p->desc));
   if (p->tile_items < 0 || p->token_items < 0 || p->token_segments < 0 || p->merge_items < 0 || p->q_rows < 0 ||
-      p->kv_rows < 0 || p->part_rows < 0 || p->q_rows > 0x7ffffeffLL || p->kv_rows > 0x7ffffeffLL)
+      p->kv_rows < 0 || p->part_rows < 0 || p->q_rows > kMaxRows || p->kv_rows > kMaxRows)
     return TLSP_ERR_INVALID_ARG;
   return TLSP_OK;
 }
