@@ -75,3 +75,37 @@ def test_memory_of_other_streams_is_kept(T, calls, plan_on, ws_on, now, plan_kep
     T.packed_attention(*tensors(3, 3), plan, ws)
     assert calls.list == ["tlsp_packed_attention"]
     assert plan.items.recorded == plan_kept and ws.buf.recorded == ws_kept
+
+
+def planned(T, q=(1, 2), kv=(1, 2), heads=4, kv_heads=2, head_dim=64, prefix_len=0, kv_starts=None):
+    return T.PackedPlan(list(q), list(kv), heads, kv_heads, head_dim, torch.float32,
+                        prefix_len=prefix_len, kv_starts=kv_starts, device="cpu")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=(2 ** 32 + 1, 1)), dict(kv=(2, 2 ** 32 + 3)), dict(q=(2 ** 31, 0)), dict(kv=(1, -2 ** 32)),
+    dict(kv_starts=[0, 2 ** 64 + 4]), dict(kv_starts=[2 ** 63, 0]), dict(prefix_len=2 ** 32 + 5),
+    dict(heads=2 ** 32 + 4), dict(kv_heads=2 ** 32 + 2), dict(head_dim=2 ** 32 + 64),
+])
+def test_numbers_that_do_not_fit(T, calls, kw):
+    """A number too large for the library's types is refused, not cut to its low bits."""
+    assert planned(T).q_rows == 3 and planned(T, q=torch.tensor([1, 2]).tolist()).kv_rows == 3
+    with pytest.raises(ValueError):
+        planned(T, **kw)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(head_dim=2 ** 32 + 64), dict(rotary_dim=2 ** 32 + 64), dict(sections=(2 ** 32 + 16, 16)),
+    dict(sections=(2 ** 32, 32)),
+])
+def test_rotary_numbers_that_do_not_fit(T, kw):
+    with pytest.raises(ValueError):
+        T.RotaryPlan(**{"head_dim": 64, **kw})
+
+
+def test_numbers_that_are_not_whole(T, calls):
+    for f in (lambda: planned(T, q=(1.5, 2)), lambda: planned(T, kv_starts=[0.5, 9]),
+              lambda: planned(T, heads=4.0), lambda: planned(T, prefix_len=3.5),
+              lambda: T.RotaryPlan(64, sections=(16.5, 15.5)), lambda: T.RotaryPlan(64.0)):
+        with pytest.raises(TypeError):
+            f()

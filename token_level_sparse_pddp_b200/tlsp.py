@@ -8,6 +8,7 @@ is missing: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 from typing import Optional, Tuple
@@ -167,6 +168,14 @@ def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.bfloat16:
         return TLSP_BF16
     raise ValueError(f"unsupported dtype {dt}")
+
+
+def _fits(value, what: str, bits: int = 32) -> int:
+    """A whole number that the library's type holds (ctypes would keep its low bits only)."""
+    n = operator.index(value)
+    if not -(1 << bits - 1) <= n < 1 << bits - 1:
+        raise ValueError(f"{what} is out of range: {n}")
+    return n
 
 
 def dims_of(Q: torch.Tensor, K: Optional[torch.Tensor] = None) -> Dims:
@@ -392,8 +401,9 @@ class RotaryPlan:
             raise ValueError(f"scaling must be one of {list(_ROTARY_SCALINGS)}")
         if amplitude is not None and not amplitude > 0:
             raise ValueError("amplitude must be positive")
-        r = head_dim if rotary_dim is None else rotary_dim
-        sec = [r // 2] if sections is None else [int(x) for x in sections]
+        head_dim = _fits(head_dim, "head_dim")
+        r = head_dim if rotary_dim is None else _fits(rotary_dim, "rotary_dim")
+        sec = [r // 2] if sections is None else [_fits(x, "a section") for x in sections]
         if not 1 <= len(sec) <= 4:
             raise ValueError("1 to 4 sections")
         desc = RotaryDesc(head_dim, r, _ROTARY_LAYOUTS[layout], len(sec),
@@ -525,13 +535,16 @@ def rotary_backward(dQ: torch.Tensor, dK: Optional[torch.Tensor], positions: tor
 
 # ----------------------------------------------------------------- packed attention
 
-def _host_ints(values, ctype):
+def _host_ints(values, ctype, what: str):
     if isinstance(values, torch.Tensor):
         if values.is_cuda:
             raise ValueError("lengths are planned on the host: pass a list or a CPU tensor")
         values = values.tolist()
     values = list(values)
-    return (ctype * len(values))(*values), len(values)
+    made = (ctype * len(values))(*values)
+    for x in (min(values), max(values)) if values else ():
+        _fits(x, what, 8 * ctypes.sizeof(ctype))
+    return made, len(values)
 
 
 class PackedPlan:
@@ -553,9 +566,12 @@ class PackedPlan:
         device = torch.device(device or "cuda")
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-        q, n = _host_ints(q_lens, ctypes.c_int32)
-        kv, n_kv = _host_ints(kv_lens, ctypes.c_int32)
-        starts, n_st = (None, n) if kv_starts is None else _host_ints(kv_starts, ctypes.c_int64)
+        heads, kv_heads = _fits(heads, "heads"), _fits(kv_heads, "kv_heads")
+        head_dim, prefix_len = _fits(head_dim, "head_dim"), _fits(prefix_len, "prefix_len")
+        q, n = _host_ints(q_lens, ctypes.c_int32, "a length")
+        kv, n_kv = _host_ints(kv_lens, ctypes.c_int32, "a length")
+        starts, n_st = (None, n) if kv_starts is None else _host_ints(kv_starts, ctypes.c_int64,
+                                                                      "a start")
         if n != n_kv or n != n_st:
             raise ValueError("q_lens, kv_lens and kv_starts must have one entry per sequence")
         if torch.cuda.is_current_stream_capturing():
