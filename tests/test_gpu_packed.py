@@ -250,6 +250,32 @@ def test_strided_tensors(T):
     assert torch.equal(T.packed_attention(Qh, Kh, Vh, plan, ws), O)
 
 
+def test_outputs_beside_inputs(T):
+    """An output among the inputs' heads or channels is taken, one on top of them refused."""
+    q, kv, h, hk, d = [70, 1, 200], [70, 1, 200], 6, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    wide = torch.randn((271, 2 * h + 2 * hk, d), generator=g, device="cuda").bfloat16()
+    Q, K, V, O = wide[:, :h], wide[:, h:h + hk], wide[:, h + hk:h + 2 * hk], wide[:, h + 2 * hk:]
+    plan = T.PackedPlan(q, kv, h, hk, d)
+    ws = plan.workspace()
+    want = T.packed_attention(Q, K, V, plan, ws)
+    before = T.launch_count()
+    for out in (Q, wide[:, 1:h + 1], wide[:, h + hk:2 * h + hk], wide[:, h + 2 * hk - 1:-1]):
+        with pytest.raises(T.TlspError) as e:
+            T.packed_attention(Q, K, V, plan, ws, out=out)
+        assert e.value.code == T.TLSP_ERR_INVALID_ARG
+    assert T.launch_count() == before
+    assert torch.equal(T.packed_attention(Q, K, V, plan, ws, out=O), want)
+    pair = torch.zeros((271, h, 2 * d), dtype=BF16, device="cuda")
+    pair[..., :d] = Q
+    T.packed_attention(pair[..., :d], K, V, plan, ws, out=pair[..., d:])
+    assert torch.equal(pair[..., d:], want) and torch.equal(pair[..., :d], Q)
+    heads_first = torch.zeros((2 * h, 271, d), dtype=BF16, device="cuda").transpose(0, 1)
+    heads_first[:, :h] = Q
+    T.packed_attention(heads_first[:, :h], K, V, plan, ws, out=heads_first[:, h:])
+    assert torch.equal(heads_first[:, h:], want)
+
+
 def test_same_bits_again(T):
     q, kv = [1] * 9 + [260], [3000 + 7 * i for i in range(9)] + [260]
     Q, K, V, Kp, Vp = inputs(q, kv, 6, 2, 128, BF16, 2000)

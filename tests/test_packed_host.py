@@ -353,3 +353,37 @@ def test_starts_whose_end_is_out_of_range(T, start, dtype):
     assert plan(0x7ffffeff - 25) == T.TLSP_OK and data.kv_rows == 0x7ffffeff
     desc.prefix_len = 0x7fffff00
     assert plan(0) == T.TLSP_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ shared memory
+
+def test_outputs_that_share_memory(T):
+    """Nothing is launched by a call whose output, lse or workspace lies on what it reads or on
+    each other."""
+    L = T.lib()
+    before = L.tlsp_launch_count()
+    data, *_ = make(T, [3, 1], [3, 900], heads=4, kv_heads=2, prefix=50)
+    base, M = 1 << 32, 1 << 24                              # addresses, never dereferenced
+    at = dict(Q=base, Kp=base + M, Vp=base + 2 * M, K=base + 3 * M, V=base + 4 * M, O=base + 5 * M,
+              lse=base + 6 * M, ws=base + 7 * M)
+
+    def call(strides=(512, 128), **kw):
+        p = {**at, **kw}
+        rows = {n: ctypes.byref(Rows(p[n], *((256, 128) if n in ("K", "V", "Kp", "Vp") else strides)))
+                for n in ("Q", "Kp", "Vp", "K", "V", "O")}
+        return L.tlsp_prefix_attention(
+            ctypes.byref(data), ctypes.c_void_p(base + 8 * M), rows["Q"], rows["Kp"], rows["Vp"],
+            rows["K"], rows["V"], rows["O"], ctypes.c_void_p(p["lse"]), 0.0, ctypes.c_void_p(p["ws"]),
+            data.ws_bytes, None)
+    for name, last in (("Q", 4 * 1024), ("Kp", 50 * 512), ("Vp", 50 * 512), ("K", 903 * 512),
+                       ("V", 903 * 512)):
+        assert call(O=at[name]) == T.TLSP_ERR_INVALID_ARG, name
+        assert call(O=at[name] + last - 16) == T.TLSP_ERR_INVALID_ARG, name
+        assert call(lse=at[name] + last - 4) == T.TLSP_ERR_INVALID_ARG, name
+        assert call(ws=at[name] - data.ws_bytes + 16) == T.TLSP_ERR_INVALID_ARG, name
+    assert call(lse=at["O"] + 16) == T.TLSP_ERR_INVALID_ARG
+    assert call(ws=at["O"]) == T.TLSP_ERR_INVALID_ARG
+    assert call(lse=at["ws"] + data.ws_bytes - 4) == T.TLSP_ERR_INVALID_ARG   # its last bytes
+    # a part of the same channels of one wider tensor
+    assert call(strides=(1024, 256), O=at["Q"] + 128) == T.TLSP_ERR_INVALID_ARG
+    assert L.tlsp_launch_count() == before

@@ -15,6 +15,7 @@
 #include <queue>
 #include <vector>
 
+#include "overlap.h"
 #include "packed.h"
 
 namespace tlsp {
@@ -730,6 +731,29 @@ int validate_output(const tlsp_rows* r, int64_t rows, int heads, int d) {
   return rows_outside || heads_outside ? TLSP_OK : TLSP_ERR_INVALID_ARG;
 }
 
+Span span_of(const tlsp_rows& r, int64_t rows, int heads, int d, int size) {
+  return Span(r.ptr, (int64_t)d * size)
+      .with(rows, (__int128)r.row_stride * size)
+      .with(heads, (__int128)r.head_stride * size);
+}
+
+// What a call writes (O, lse, its workspace) shares no memory with what it reads, nor with
+// each other: other items still read their queries and keys while one's rows are written.
+int validate_overlap(const PackedArgs& a, int size, size_t ws_bytes) {
+  const Span O = span_of(a.O, a.q_rows, a.heads, a.d, size);
+  const Span lse(a.lse, a.lse ? a.q_rows * a.heads * (int64_t)sizeof(float) : 0);
+  const Span ws(a.status, (int64_t)ws_bytes);
+  if (!apart(O, lse) || !apart(O, ws) || !apart(lse, ws)) return TLSP_ERR_INVALID_ARG;
+  const Span read[] = {span_of(a.Q, a.q_rows, a.heads, a.d, size),
+                       span_of(a.K, a.kv_rows, a.kv_heads, a.d, size),
+                       span_of(a.V, a.kv_rows, a.kv_heads, a.d, size),
+                       span_of(a.Kp, a.prefix_len, a.kv_heads, a.d, size),
+                       span_of(a.Vp, a.prefix_len, a.kv_heads, a.d, size)};
+  for (const Span& r : read)
+    if (!apart(O, r) || !apart(lse, r) || !apart(ws, r)) return TLSP_ERR_INVALID_ARG;
+  return TLSP_OK;
+}
+
 // Strides of axes of length 1 are never used: set to something valid.
 tlsp_rows tidy(const tlsp_rows* r, int64_t rows, int heads, int d) {
   tlsp_rows t{};
@@ -801,6 +825,7 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   a.status = reinterpret_cast<int*>(base);
   a.part_lse = reinterpret_cast<float*>(base + L.lse);
   a.part_o = reinterpret_cast<float*>(base + L.o);
+  TLSP_TRY(validate_overlap(a, size, L.total));
   cudaStream_t st = (cudaStream_t)stream;
   if (bf16) {
     if (a.n_tiles > 0) TLSP_TRY(packed_tile(a, st));

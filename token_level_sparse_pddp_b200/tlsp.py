@@ -672,7 +672,8 @@ def packed_attention(Q, K, V, plan: PackedPlan, ws: Workspace, scale: Optional[f
     kv_starts), any strides that are multiples of 16 bytes with contiguous channels. lse, if
     given (fp32 [tokens, heads]), receives each row's log partition; rows that see no key get
     O = 0 and lse = -inf. Rows of a given `out` (and lse) behind the last sequence are left as
-    they are; without `out` they are zero.
+    they are; without `out` they are zero. `out` and lse may share no memory with an input or
+    each other (not out=Q): other parts of one wider tensor may be used.
     """
     if plan.prefix_len:
         raise ValueError("the plan has a prefix: call prefix_attention")
