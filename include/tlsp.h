@@ -290,7 +290,8 @@ int tlsp_rotary_make_plan(const tlsp_rotary_desc* desc, tlsp_rotary_plan* plan);
  * axes: strides in elements, channels contiguous. */
 typedef struct {
   const void* in;
-  void* out; /* may be `in` itself with the same strides (in place); no other overlap */
+  void* out; /* may be `in` itself with the same strides (in place); shares no other memory with
+              * an input or output, nor its own elements: TLSP_ERR_INVALID_ARG */
   int64_t in_batch, in_token, in_head;
   int64_t out_batch, out_token, out_head;
   int32_t heads;

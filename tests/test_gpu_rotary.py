@@ -113,6 +113,41 @@ def test_strides_and_in_place(T, dtype, d, r):
     assert torch.equal(odd, T.rotary(src.contiguous(), None, pos, plan))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_outputs_beside_inputs(T, dtype):
+    """Outputs in other parts of the inputs' tensor, and in place where only axes of length 1 have
+    other strides; outputs on other inputs are refused."""
+    n, h, d = 130, 3, 64
+    pos = torch.arange(n, device="cuda")
+    plan = T.RotaryPlan(d)
+    wide = rand((n, 4 * h, d), dtype)
+    parts = [wide[:, i * h:(i + 1) * h] for i in range(4)]
+    want = T.rotary(parts[0], parts[1], pos, plan)
+    before = T.launch_count()
+    for out in ((parts[1], parts[0]), (parts[2], parts[2]), (parts[0], parts[0]), (parts[2], parts[0]),
+                (wide[:, 1:h + 1], parts[3]), (parts[2], wide[:, 3 * h - 1:-1])):
+        with pytest.raises(T.TlspError) as e:
+            T.rotary(parts[0], parts[1], pos, plan, out=out)
+        assert e.value.code == T.TLSP_ERR_INVALID_ARG
+    assert T.launch_count() == before
+    T.rotary(parts[0], parts[1], pos, plan, out=(parts[3], parts[2]))
+    assert torch.equal(parts[3], want[0]) and torch.equal(parts[2], want[1])
+    T.rotary(parts[0], parts[1], pos, plan, out=(parts[0], parts[3]))       # one of them in place
+    assert torch.equal(parts[0], want[0]) and torch.equal(parts[3], want[1])
+    pairs = rand((n, h, 2, d), dtype, 1)                                    # heads in turn
+    want = T.rotary(pairs[:, :, 0], pairs[:, :, 1], pos, plan)
+    T.rotary(pairs[:, :, 0], pairs[:, :, 1], pos, plan, out=(pairs[:, :, 0], pairs[:, :, 1]))
+    assert torch.equal(pairs[:, :, 0], want[0]) and torch.equal(pairs[:, :, 1], want[1])
+    three = rand((2, 3, h, n, d), dtype, 2)                                 # [batch, q/k/v, heads, ...]
+    want = T.rotary(three[:, 0], three[:, 1], pos, plan)
+    T.rotary(three[:, 0], three[:, 1], pos, plan, out=(three[:, 0], three[:, 1]))
+    assert torch.equal(three[:, 0], want[0]) and torch.equal(three[:, 1], want[1])
+    x = rand((1, h, n, d), dtype, 3)
+    want = T.rotary(x, None, pos, plan)
+    T.rotary(x, None, pos, plan, out=x.as_strided(x.shape, (7 * d, *x.stride()[1:])))
+    assert torch.equal(x, want)
+
+
 def test_backward_is_the_gradient(T):
     """Against differences of the forward pass: the map is linear, so <y(x + e) - y(x), g> is
     <e, gradient> up to the roundings of fp32 (n terms of a sum taken in 64 bits, each

@@ -387,3 +387,31 @@ def test_outputs_that_share_memory(T):
     # a part of the same channels of one wider tensor
     assert call(strides=(1024, 256), O=at["Q"] + 128) == T.TLSP_ERR_INVALID_ARG
     assert L.tlsp_launch_count() == before
+
+
+def test_rotary_outputs_that_share_memory(T):
+    """An output is its own input or lies apart from everything else."""
+    L = T.lib()
+    before = L.tlsp_launch_count()
+    plan = T.RotaryPlan(128).data
+    A, B, C, D = (x << 32 for x in range(1, 5))             # addresses, never dereferenced
+    token = 4 * 128
+
+    def call(q, k=None, batch=1, tokens=40):
+        c = RotaryCall(batch, tokens, 1, 0, 0x10000, 0, 0)
+        return L.tlsp_rotary(ctypes.byref(plan), ctypes.byref(c), ctypes.byref(q),
+                             None if k is None else ctypes.byref(k), 0, None)
+
+    def t(src, dst, src_strides=(0, token, 128), dst_strides=(0, token, 128), heads=4):
+        return RotaryTensor(src, dst, *src_strides, *dst_strides, heads)
+    for q, k in (
+            (t(A, A + 256), None), (t(A, A + 2 * token), None), (t(A, A - 2 * token), None),
+            (t(A, A + 39 * 2 * token), None),               # the last token's row
+            (t(A, A, dst_strides=(0, 128, 40 * 128)), None),
+            (t(A, B, dst_strides=(0, token, 64)), None),    # heads on each other
+            (t(A, B, dst_strides=(0, 0, 128)), None), (t(A, B, dst_strides=(0, 256, 128)), None),
+            (t(A, B), t(C, B)), (t(A, B), t(B, C)), (t(A, B), t(B, A)), (t(A, A), t(A, A)),
+            (t(A, A), t(C, A + 256)), (t(A, C), t(C + 16, D))):
+        assert call(q, k) == T.TLSP_ERR_INVALID_ARG, (q.src, q.dst)
+    assert call(t(A, B, dst_strides=(token, token, 128)), batch=2) == T.TLSP_ERR_INVALID_ARG
+    assert L.tlsp_launch_count() == before

@@ -22,6 +22,7 @@
 #include <cmath>
 
 #include "kernels.h"
+#include "overlap.h"
 
 namespace tlsp {
 namespace {
@@ -280,9 +281,36 @@ int validate_plan(const tlsp_rotary_plan* p) {
 int validate_tensor(const tlsp_rotary_tensor* t, int size) {
   if (!t->in || !t->out || t->heads < 1) return TLSP_ERR_INVALID_ARG;
   if ((uintptr_t)t->in % size || (uintptr_t)t->out % size) return TLSP_ERR_INVALID_ARG;
-  if (t->in == t->out && (t->in_batch != t->out_batch || t->in_token != t->out_token ||
-                          t->in_head != t->out_head))
-    return TLSP_ERR_INVALID_ARG;
+  return TLSP_OK;
+}
+
+// A thread writes its heads of a token while others still read theirs: an output shares
+// memory with its own input only if it is that input, else with no input and no output, and
+// its own elements lie apart.
+int validate_overlap(const RotaryParams& p, int count, int size) {
+  auto span = [&](const void* at, int64_t batch, int64_t token, int64_t head, int heads) {
+    return Span(at, (int64_t)p.plan.head_dim * size)
+        .with(p.batch, (__int128)batch * size)
+        .with(p.tokens, (__int128)token * size)
+        .with(heads, (__int128)head * size);
+  };
+  auto in = [&](const tlsp_rotary_tensor& t) {
+    return span(t.in, t.in_batch, t.in_token, t.in_head, t.heads);
+  };
+  auto out = [&](const tlsp_rotary_tensor& t) {
+    return span(t.out, t.out_batch, t.out_token, t.out_head, t.heads);
+  };
+  for (int x = 0; x < count; ++x) {
+    const tlsp_rotary_tensor& t = p.t[x];
+    const Span o = out(t);
+    if (!o.distinct()) return TLSP_ERR_INVALID_ARG;
+    const bool in_place = t.in == t.out && (p.batch == 1 || t.in_batch == t.out_batch) &&
+                          (p.tokens == 1 || t.in_token == t.out_token) &&
+                          (t.heads == 1 || t.in_head == t.out_head);
+    if (!in_place && !apart(o, in(t))) return TLSP_ERR_INVALID_ARG;
+    if (count == 2 && (!apart(o, in(p.t[1 - x])) || !apart(o, out(p.t[1 - x]))))
+      return TLSP_ERR_INVALID_ARG;
+  }
   return TLSP_OK;
 }
 
@@ -370,6 +398,7 @@ int tlsp_rotary(const tlsp_rotary_plan* plan, const tlsp_rotary_call* call,
   p.sign = backward ? -1.f : 1.f;
   p.t[0] = *Q;
   if (K) p.t[1] = *K;
+  TLSP_TRY(validate_overlap(p, K ? 2 : 1, size));
   cudaStream_t st = (cudaStream_t)stream;
   return call->dtype == TLSP_BF16 ? launch<__nv_bfloat16>(p, *call, K != nullptr, st)
                                   : launch<float>(p, *call, K != nullptr, st);

@@ -522,7 +522,8 @@ def rotary(Q: torch.Tensor, K: Optional[torch.Tensor], positions: torch.Tensor, 
                contiguous channels (slices of a fused projection, for instance)
     positions  int32 or int64 [tokens] or [batch, tokens]; with several sections [axes, tokens]
                or [axes, batch, tokens]
-    out        tensors to write (the inputs themselves: in place)
+    out        tensors to write: each its own input (in place), or memory that no input or other
+               output lies in (other parts of one wider tensor may be used)
     """
     return _rotary(Q, K, positions, plan, out, 0)
 
