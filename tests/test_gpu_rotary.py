@@ -188,6 +188,51 @@ def test_gradient_against_the_formula(T):
         near(T.rotary_backward(g, None, pos, plan), (x.grad, tol))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_autograd(T, dtype):
+    """Gradients through rotary() are rotary_backward()'s: of Q and K, of slices of a fused tensor,
+    of a broadcast input (summed), of either alone, on another stream and in a captured step."""
+    n, h, hk, d = 70, 4, 2, 128
+    pos = torch.randint(0, 5000, (n,), device="cuda")
+    plan = T.RotaryPlan(d, rotary_dim=64, scaling="linear", factor=2.0)
+    gq, gk = rand((n, h, d), dtype, 1), rand((n, hk, d), dtype, 2)
+    want = T.rotary_backward(gq, gk, pos, plan)
+    qkv = rand((n, h + 2 * hk, d), dtype).requires_grad_()
+
+    def step():
+        Q, K = T.rotary(qkv[:, :h], qkv[:, h:h + hk], pos, plan)
+        return torch.autograd.grad((Q, K), qkv, (gq, gk))[0]
+
+    def same(grad):
+        assert torch.equal(grad[:, :h], want[0]) and torch.equal(grad[:, h:h + hk], want[1])
+        assert not grad[:, h + hk:].any()
+    same(step())
+    x = rand((n, 1, d), FP32, 3).to(dtype).requires_grad_()
+    y = T.rotary(x.expand(n, h, d), None, pos, plan)
+    dx, = torch.autograd.grad(y, x, gq)
+    assert torch.equal(dx, want[0].sum(1, keepdim=True))
+    k = rand((n, hk, d), dtype, 4).requires_grad_()
+    Q, K = T.rotary(gq, k, pos, plan)
+    assert torch.equal(torch.autograd.grad(K.sum(), k)[0],
+                       T.rotary_backward(torch.ones_like(k), None, pos, plan))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            got = step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            captured = step()
+    side.synchronize()
+    same(got)
+    captured.zero_()
+    gq.copy_(rand((n, h, d), dtype, 7))
+    want = T.rotary_backward(gq, gk, pos, plan)
+    graph.replay()
+    torch.cuda.synchronize()
+    same(captured)
+
+
 def test_special_values_stay_in_their_pair(T):
     n, h, d = 64, 2, 128
     x = rand((n, h, d), BF16)

@@ -109,3 +109,68 @@ def test_numbers_that_are_not_whole(T, calls):
               lambda: T.RotaryPlan(64, sections=(16.5, 15.5)), lambda: T.RotaryPlan(64.0)):
         with pytest.raises(TypeError):
             f()
+
+
+# ------------------------------------------------------------------ gradients
+
+def turned(T, x, pos, plan, sign=1.0):
+    """The formula for one axis and the half layout, in elementary operations."""
+    r = plan.rotary_dim
+    turns = torch.tensor([plan.data.turns[i] / 2.0 ** 64 for i in range(r // 2)], dtype=torch.float64)
+    a = 2 * torch.pi * pos.double()[:, None] * turns
+    c, s = (plan.data.amplitude * a.cos())[:, None], (sign * plan.data.amplitude * a.sin())[:, None]
+    x1, x2 = x.double()[..., :r // 2], x.double()[..., r // 2:r]
+    return torch.cat([x1 * c - x2 * s, x2 * c + x1 * s, x.double()[..., r:]], -1)
+
+
+@pytest.fixture
+def on_host(T, monkeypatch):
+    """rotary()'s launch replaced by the formula: the autograd path without a GPU."""
+    def fake(Q, K, positions, plan, out, backward):
+        made = [turned(T, x.detach(), positions, plan, -1.0 if backward else 1.0).to(x.dtype)
+                for x in (Q, K) if x is not None]
+        return made[0] if K is None else tuple(made)
+    monkeypatch.setattr(T, "_rotary", fake)
+
+
+def test_rotary_carries_gradients(T, on_host):
+    """rotary() of tensors that require gradients returns ones that carry them; so does
+    rotary_backward(), whose own gradient turns forward again."""
+    plan = T.RotaryPlan(64, rotary_dim=32)
+    pos = torch.tensor([3, 0, 70])
+    g = torch.Generator().manual_seed(0)
+    q, k, gq, gk = (torch.randn(3, h, 64, generator=g, dtype=torch.float64) for h in (2, 1, 2, 1))
+    for need_q, need_k in ((True, True), (True, False), (False, True)):
+        Q, K = q.clone().requires_grad_(need_q), k.clone().requires_grad_(need_k)
+        yq, yk = T.rotary(Q, K, pos, plan)
+        ((yq * gq).sum() + (yk * gk).sum()).backward()
+        for x, grad, need in ((Q, gq, need_q), (K, gk, need_k)):
+            assert (x.grad is not None) == need
+            if need:
+                assert torch.allclose(x.grad, turned(T, grad, pos, plan, -1.0), rtol=0, atol=1e-12)
+    # one output alone takes part; broadcast gradients (of a sum)
+    Q, K = q.clone().requires_grad_(), k.clone().requires_grad_()
+    T.rotary(Q, K, pos, plan)[1].sum().backward()
+    assert torch.allclose(K.grad, turned(T, torch.ones_like(k), pos, plan, -1.0), rtol=0, atol=1e-12)
+    assert Q.grad is None or not Q.grad.any()
+    Q = q.clone().requires_grad_()
+    assert torch.autograd.gradcheck(lambda x: T.rotary(x, None, pos, plan), Q)
+    assert torch.autograd.gradcheck(lambda x: T.rotary_backward(x, None, pos, plan), Q)
+    assert torch.autograd.gradgradcheck(lambda x: T.rotary(x, None, pos, plan) ** 2, Q)
+    with torch.no_grad():
+        assert not T.rotary(Q, None, pos, plan).requires_grad
+    assert not T.rotary(q, k, pos, plan)[0].requires_grad
+
+
+def test_given_outputs_carry_no_gradients(T, on_host):
+    """A gradient could not flow through memory that the caller gives: refused, unless none is
+    asked for."""
+    plan, pos = T.RotaryPlan(64), torch.arange(3)
+    x, y = torch.zeros(3, 2, 64, requires_grad=True), torch.zeros(3, 2, 64)
+    for q, k, out in ((x, None, y), (x, None, x), (y, None, x), (y, x, (y, x)), (y, y, (y, x))):
+        with pytest.raises(ValueError):
+            T.rotary(q, k, pos, plan, out=out)
+        with pytest.raises(ValueError):
+            T.rotary_backward(q, k, pos, plan, out=out)
+        with torch.no_grad():
+            T.rotary(q, k, pos, plan, out=out)

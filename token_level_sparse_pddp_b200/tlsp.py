@@ -514,6 +514,43 @@ def _rotary(Q, K, positions, plan: RotaryPlan, out, backward: int):
     return q_out if K is None else (q_out, k_out)
 
 
+class _RotaryGrad(torch.autograd.Function):
+    """_rotary with its gradient, which is the transposed map (and whose own is the map again)."""
+
+    @staticmethod
+    def forward(ctx, Q, K, positions, plan, backward):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.plan, ctx.turned = plan, backward
+        return _rotary(Q, K, positions, plan, None, backward)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        positions, = ctx.saved_tensors
+        g = [None if x is None or not need else x if x.stride(-1) == 1 else x.contiguous()
+             for x, need in zip(grads, ctx.needs_input_grad)]
+        there = [x for x in g if x is not None]
+        if there:
+            d = _turn(there[0], there[1] if len(there) > 1 else None, positions, ctx.plan, None,
+                      1 - ctx.turned)
+            d = iter(d if len(there) > 1 else (d,))
+            g = [None if x is None else next(d) for x in g]
+        return (*g, *[None] * (5 - len(g)))
+
+
+def _turn(Q, K, positions, plan: RotaryPlan, out, backward: int):
+    wanted = Q.requires_grad or (K is not None and K.requires_grad)
+    if out is not None:
+        for x in (out,) if K is None else out:
+            wanted = wanted or x.requires_grad
+    if wanted and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("a given `out` carries no gradient: call without it, or under "
+                             "torch.no_grad()")
+        return _RotaryGrad.apply(Q, K, positions, plan, backward)
+    return _rotary(Q, K, positions, plan, out, backward)
+
+
 def rotary(Q: torch.Tensor, K: Optional[torch.Tensor], positions: torch.Tensor, plan: RotaryPlan,
            out=None):
     """Rotates queries and keys of the same tokens in one launch -> (Q', K') (Q' if K is None).
@@ -524,14 +561,16 @@ def rotary(Q: torch.Tensor, K: Optional[torch.Tensor], positions: torch.Tensor, 
                or [axes, batch, tokens]
     out        tensors to write: each its own input (in place), or memory that no input or other
                output lies in (other parts of one wider tensor may be used)
+
+    Carries gradients to Q and K (not with `out`).
     """
-    return _rotary(Q, K, positions, plan, out, 0)
+    return _turn(Q, K, positions, plan, out, 0)
 
 
 def rotary_backward(dQ: torch.Tensor, dK: Optional[torch.Tensor], positions: torch.Tensor,
                     plan: RotaryPlan, out=None):
     """Gradients of rotary()'s inputs from those of its outputs (the transposed map)."""
-    return _rotary(dQ, dK, positions, plan, out, 1)
+    return _turn(dQ, dK, positions, plan, out, 1)
 
 
 # ----------------------------------------------------------------- packed attention
