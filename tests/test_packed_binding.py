@@ -174,3 +174,26 @@ def test_given_outputs_carry_no_gradients(T, on_host):
             T.rotary_backward(q, k, pos, plan, out=out)
         with torch.no_grad():
             T.rotary(q, k, pos, plan, out=out)
+
+
+def test_attention_has_no_gradient(T, calls):
+    """The attention calls have no backward pass and say so instead of returning a result that
+    carries none."""
+    Q, K, V = tensors(3, 3)
+    ws = workspace(T, 5)
+    prefix = torch.zeros(4, 2, 64)
+    for which in range(3):
+        args = [Q, K, V]
+        args[which] = args[which].clone().requires_grad_()
+        with pytest.raises(ValueError):
+            T.packed_attention(*args, plan_of(T, [3], [3]), ws)
+        with torch.no_grad():
+            T.packed_attention(*args, plan_of(T, [3], [3]), ws)
+    for which in range(2):
+        pre = [prefix, prefix]
+        pre[which] = prefix.clone().requires_grad_()
+        with pytest.raises(ValueError):
+            T.prefix_attention(Q, *pre, K, V, plan_of(T, [3], [3], prefix=4), ws)
+    with pytest.raises(ValueError):
+        T.packed_attention(Q, K, V, plan_of(T, [3], [3]), ws, out=Q.clone().requires_grad_())
+    assert len(calls.list) == 3

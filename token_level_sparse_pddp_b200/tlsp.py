@@ -656,6 +656,9 @@ def _packed_rows(t: Optional[torch.Tensor], what: str, rows: int, heads: int, pl
     s0, s1, s2 = t.stride()
     if s2 != 1:
         raise ValueError(f"{what}: channels must be contiguous")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, and packed attention has no backward pass: "
+                         "call it under torch.no_grad()")
     return _ROWS.pack(t.data_ptr(), s0, s1)
 
 
@@ -713,7 +716,8 @@ def packed_attention(Q, K, V, plan: PackedPlan, ws: Workspace, scale: Optional[f
     given (fp32 [tokens, heads]), receives each row's log partition; rows that see no key get
     O = 0 and lse = -inf. Rows of a given `out` (and lse) behind the last sequence are left as
     they are; without `out` they are zero. `out` and lse may share no memory with an input or
-    each other (not out=Q): other parts of one wider tensor may be used.
+    each other (not out=Q): other parts of one wider tensor may be used. No backward pass: tensors
+    that require gradients are refused unless gradients are switched off.
     """
     if plan.prefix_len:
         raise ValueError("the plan has a prefix: call prefix_attention")
