@@ -197,3 +197,15 @@ def test_attention_has_no_gradient(T, calls):
     with pytest.raises(ValueError):
         T.packed_attention(Q, K, V, plan_of(T, [3], [3]), ws, out=Q.clone().requires_grad_())
     assert len(calls.list) == 3
+
+
+# ------------------------------------------------------------------ scale
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-60, -1e-50, 7e-46])
+def test_scales_that_are_zero_in_32_bits(T, calls, scale):
+    """The library takes a scale of 0 for 1/sqrt(d), so none may become 0 on its way there."""
+    ws = workspace(T, 5)
+    with pytest.raises(ValueError):
+        T.packed_attention(*tensors(3, 3), plan_of(T, [3], [3]), ws, scale=scale)
+    T.packed_attention(*tensors(3, 3), plan_of(T, [3], [3]), ws, scale=1e-44)
+    assert len(calls.list) == 1

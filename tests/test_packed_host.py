@@ -415,3 +415,14 @@ def test_rotary_outputs_that_share_memory(T):
         assert call(q, k) == T.TLSP_ERR_INVALID_ARG, (q.src, q.dst)
     assert call(t(A, B, dst_strides=(token, token, 128)), batch=2) == T.TLSP_ERR_INVALID_ARG
     assert L.tlsp_launch_count() == before
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3e38, 3.4e38])
+def test_scales_beyond_the_range_of_the_exponent(T, scale):
+    """Kernels work with scale log2(e): its product has to be finite too."""
+    L = T.lib()
+    data, *_ = make(T, [3, 1], [3, 900], heads=4, kv_heads=2)
+    rows = [ctypes.byref(Rows(x << 32, h * 128, 128)) for x, h in ((1, 4), (2, 2), (3, 2), (4, 4))]
+    assert L.tlsp_packed_attention(ctypes.byref(data), ctypes.c_void_p(5 << 32), *rows, None, scale,
+                                   ctypes.c_void_p(6 << 32), data.ws_bytes, None) == \
+        T.TLSP_ERR_INVALID_ARG

@@ -780,7 +780,7 @@ int attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* 
   const tlsp_packed_desc& d = plan->desc;
   const bool bf16 = d.dtype == TLSP_BF16;
   const int size = bf16 ? 2 : 4;
-  if (!(std::fabs(scale) < INFINITY)) return TLSP_ERR_INVALID_ARG;
+  if (!(std::fabs(scale * 1.4426950408889634f) < INFINITY)) return TLSP_ERR_INVALID_ARG;  // as the kernels take it
   TLSP_TRY(validate_rows(Q, plan->q_rows, d.heads, d.head_dim, size));
   TLSP_TRY(validate_rows(O, plan->q_rows, d.heads, d.head_dim, size));
   TLSP_TRY(validate_output(O, plan->q_rows, d.heads, d.head_dim));

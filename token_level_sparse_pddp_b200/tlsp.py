@@ -682,8 +682,8 @@ def _packed(Q, Kp, Vp, K, V, plan: PackedPlan, ws: Workspace, scale, out, lse):
         raise ValueError(f"the workspace must live on {plan.device}")
     if scale is None:
         scale = 0.0
-    elif scale == 0.0:
-        raise ValueError("scale must not be 0")
+    elif abs(scale) < 2.0 ** -149:  # 0 for the library: 1/sqrt(d)
+        raise ValueError("scale must not be 0 in 32 bits")
     here = torch._C._cuda_getCurrentRawStream(dev)
     if (here != plan._made_on or here != ws.made_on) and \
             not torch.cuda.is_current_stream_capturing():
