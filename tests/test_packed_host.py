@@ -426,3 +426,18 @@ def test_scales_beyond_the_range_of_the_exponent(T, scale):
     assert L.tlsp_packed_attention(ctypes.byref(data), ctypes.c_void_p(5 << 32), *rows, None, scale,
                                    ctypes.c_void_p(6 << 32), data.ws_bytes, None) == \
         T.TLSP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_merges_that_no_grid_holds(T, dtype):
+    """More heads than the merging kernel's grid takes are refused by the plan, not by a call
+    that has launched part of its work."""
+    data = T.PackedPlanData()
+    q, kv = (ctypes.c_int32 * 9)(*[1] * 9), (ctypes.c_int32 * 9)(*[5] * 9)
+
+    def plan(heads, kv_heads):
+        desc = T.PackedDesc(9, heads, kv_heads, 64, dtype, 1, 999)
+        return T.lib().tlsp_packed_make_plan(ctypes.byref(desc), q, kv, None, None, 0,
+                                             ctypes.byref(data))
+    assert plan(4 * 65535, 65535) == T.TLSP_ERR_WORKSPACE and data.merge_items == 9
+    assert plan(5 * 65535, 65535) == T.TLSP_ERR_UNSUPPORTED

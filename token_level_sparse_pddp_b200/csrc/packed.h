@@ -48,6 +48,16 @@ static_assert(sizeof(MergeItem) == 32, "item table layout");
 
 constexpr int kTokenRows = 16;    // rows (tokens x heads of a group) of a token item
 constexpr int kMergeTokens = 1;   // tokens of a merge item
+constexpr int kMergeWarps = 4;    // of a block of the merge kernel
+constexpr int kMergeAhead = 8;    // parts in flight for a warp
+
+// With more parts than a warp has in flight, a block's warps share a row's.
+inline bool merge_joint(int parts) { return parts > kMergeAhead; }
+// Blocks (the grid's y) that the rows of a merge item take.
+inline int64_t merge_blocks(int heads, int parts) {
+  return ceil_div((int64_t)kMergeTokens * heads, merge_joint(parts) ? 1 : kMergeWarps);
+}
+constexpr int kMaxGridY = 65535;
 
 constexpr int kMaxSegments = 32;  // of a token item: its tokens' sequences and the prefix
 constexpr int kMaxCluster = 8;    // CTAs that share a token item (portable cluster size)

@@ -14,8 +14,7 @@
 namespace tlsp {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kAhead = 8;  // parts in flight for a warp
+constexpr int kWarps = kMergeWarps, kAhead = kMergeAhead;
 
 template <int D>
 struct Row;  // a lane's channels of a row
@@ -144,11 +143,10 @@ __global__ void __launch_bounds__(32 * kWarps)
 
 template <class T>
 int merge(const PackedArgs& a, cudaStream_t st) {
-  // More parts than a warp has in flight: the block's warps share them.
-  const bool joint = a.merge_parts > kAhead;
-  const dim3 grid((unsigned)a.n_merges,
-                  (unsigned)ceil_div((int64_t)kMergeTokens * a.heads, joint ? 1 : kWarps));
-  if (grid.y > 65535) return TLSP_ERR_UNSUPPORTED;
+  const bool joint = merge_joint(a.merge_parts);
+  const int64_t blocks = merge_blocks(a.heads, a.merge_parts);
+  if (blocks > kMaxGridY) return TLSP_ERR_UNSUPPORTED;  // (the planner refuses such plans)
+  const dim3 grid((unsigned)a.n_merges, (unsigned)blocks);
   auto go = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * kWarps, 0, 1, st, a); };
   if (joint) return a.d == 128 ? go(packed_merge_kernel<T, 128, true>) : go(packed_merge_kernel<T, 64, true>);
   return a.d == 128 ? go(packed_merge_kernel<T, 128, false>) : go(packed_merge_kernel<T, 64, false>);

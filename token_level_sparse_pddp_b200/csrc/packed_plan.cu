@@ -197,6 +197,8 @@ class Planner {
         std::max({tiles.size(), tokens.size(), token_items.size() * (size_t)cluster, merges.size()}) *
         (uint64_t)d_.kv_heads;
     if (most_items > 0x7fffffffLL) return TLSP_ERR_UNSUPPORTED;
+    for (const MergeItem& t : merges) merge_parts = std::max(merge_parts, t.a_parts + t.b_parts);
+    if (!merges.empty() && merge_blocks(d_.heads, merge_parts) > kMaxGridY) return TLSP_ERR_UNSUPPORTED;
     return TLSP_OK;
   }
 
@@ -205,6 +207,7 @@ class Planner {
   std::vector<TokenSegment> segments;
   std::vector<MergeItem> merges;
   int cluster = 1;
+  int merge_parts = 0;  // most parts of a merge item
   int64_t q_rows = 0, kv_rows = 0;
   int64_t part_rows() const { return part_rows_; }
 
@@ -858,8 +861,7 @@ int tlsp_packed_make_plan(const tlsp_packed_desc* desc, const int32_t* q_lens,
     out.token_items = (int32_t)(p.tokens.size() + p.token_items.size());
     out.token_segments = (int32_t)p.segments.size();
     out.cluster = p.cluster;
-    for (const MergeItem& t : p.merges)
-      out.merge_parts = std::max(out.merge_parts, t.a_parts + t.b_parts);
+    out.merge_parts = p.merge_parts;
     out.merge_items = (int32_t)p.merges.size();
     out.q_rows = p.q_rows;
     out.kv_rows = p.kv_rows;
