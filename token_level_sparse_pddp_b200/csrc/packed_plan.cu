@@ -144,15 +144,11 @@ class Planner {
       }
     }
     // prefix work of at most kTokenRows rows goes to the token kernel
-    std::vector<PackedItem> shared_tokens;
-    for (size_t i = 0; i < shared.size();) {
-      if (shared[i].nt * group_ <= kTokenRows) {
-        shared_tokens.push_back(shared[i]);
-        shared.erase(shared.begin() + (std::ptrdiff_t)i);
-      } else {
-        ++i;
-      }
-    }
+    const auto few_rows = std::stable_partition(
+        shared.begin(), shared.end(),
+        [&](const PackedItem& t) { return (int64_t)t.nt * group_ > kTokenRows; });
+    const std::vector<PackedItem> shared_tokens(few_rows, shared.end());
+    shared.erase(few_rows, shared.end());
     const std::vector<int64_t> cut = tile_split(whole, shared, shared_tokens);
     std::vector<Piece> own_parts;
     for (size_t x = 0; x < whole.size(); ++x) {
