@@ -371,7 +371,7 @@ typedef struct {
 
 /* O (and lse fp32 [q_rows, heads], natural log, if not NULL) of the packed
  * sequences of a plan without prefix. `items` is the device copy of the item
- * table (16-byte aligned). scale multiplies q . k (0: 1/sqrt(d)). Rows of O
+ * table (16-byte aligned), read in the order of the stream. scale multiplies q . k (0: 1/sqrt(d)). Rows of O
  * and lse behind the last sequence are not written. O, lse and ws share no
  * memory with an input or each other (O may lie among an input's heads or
  * channels, as another part of one tensor), nor O's rows and heads with each

@@ -10,9 +10,11 @@
 // filled by 16-byte cp.async while the other is used: V(j) comes in under Q K(j)^T,
 // K(j + 1) under P V(j).
 // Measured, six ragged sequences (1850 tokens, 2989 keys, 8 / 2 heads, d = 64):
-// 65.5 us = 23 TFLOP/s, with the merge; 8 x 1024 queries and keys without mask 35 TFLOP/s (packed FMAs
-// alone reach 64 in a loop on registers; shared-memory wavefronts are 74% busy, the
-// FMA pipe 57%; 64-row items and 8 rows per thread measured within 3% of this).
+// 65.8 us = 23 TFLOP/s, with the merge; 8 x 1024 queries and keys without mask 35 TFLOP/s
+// (packed FMAs alone reach 64 in a loop on registers; shared-memory wavefronts are 74%
+// busy, the FMA pipe 57%; 64-row items and 8 rows per thread measured within 3% of this).
+// 64 single tokens of 12 / 4 heads of 128 behind 4000 to 20000 keys each: 1160 us = 2.7
+// TB/s, as 3 of an item's 16 rows are filled (22 TFLOP/s with the others counted).
 // A masked key has weight 0, and 0 x inf is NaN: rows behind the key range are stored
 // as zeros, and a block that only part of the rows see is searched for values that are
 // not finite; with one, masked products are skipped.

@@ -683,8 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 8; ++q) any_odd |= bars.odd[k & 1][q];
       // Each thread writes its half of the row from its registers, eight channels at a time:
       // wider steps, and rows staged in shared memory for stores of whole lines, cost
-      // registers that the chunk loop then lacks (24 ragged prompts 201 us, 16384 tokens
-      // of 12 heads of 64 492 us; 16 channels: 201 and 536 us; staged: 205 and 505 us).
+      // registers that the chunk loop then lacks (on a cool GPU, in turns: 24 ragged prompts
+      // 201 us, 16384 tokens of 12 heads of 64 492 us; 16 channels: 201 and 536 us; staged:
+      // 205 and 505 us. Back to back, at the power limit, the prompts take 237 us).
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.O.ptr) +
                            (int64_t)(it.q0 + i) * p.a.O.row_stride +
                            (int64_t)head * p.a.O.head_stride + half * kCols;

@@ -11,9 +11,10 @@
 // maximum, sum and output in registers and no barrier between warps until the four
 // partial outputs are joined in shared memory, and those of the cluster's CTAs
 // through each other's: a batch of single tokens takes one launch (8 tokens behind
-// 21758 cached keys, 4 heads of 128, 45 MB: 13.2 us, of which 3.7 us until the first
-// keys are there and 2.5 us to join; two launches, with a kernel that merged the parts
-// of independent CTAs: 13.4 us, and 3 us more on the host).
+// 21758 cached keys, 4 heads of 128, 45 MB: 13.6 us on replay, of which some 4 us until
+// the first keys are there and 2.5 us to join; two launches, with a kernel that merged the
+// parts of independent CTAs, were 0.2 us slower, and 3 us more on the host). 64 channels:
+// 10.9 us; 64 tokens of 4000 to 20000 keys 278 us = 5.6 TB/s.
 // 64 tokens x 8 groups of 16 to 2000 keys: 41 us = 5.3 TB/s alone. Behind tile items
 // (whose kernel lets it start at once) its CTAs take the SMs that those do not fill.
 // The reference maximum of a row is raised only when a score passes it by more

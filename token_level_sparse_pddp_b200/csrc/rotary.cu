@@ -4,10 +4,11 @@
 // sin a) with a = p w. The transposed map (the backward pass) turns by -a.
 //
 // Angles: the plan holds w / 2 pi modulo 1 as a 64-bit fraction F of a turn, so
-// p F modulo 2^64 is the angle in turns, reduced exactly for every 64-bit
-// position (the frequency's own rounding, 2^-65 of a turn, times p is the only
-// error: 2^-34 of a turn at p = 2^31). Its top 32 bits as a signed number
-// over 2^31 are the angle in half turns in [-1, 1), which sincospi takes.
+// p F modulo 2^64 is the angle in turns, reduced without an error of its own for every
+// 64-bit position. Its top 32 bits as a signed number over 2^31 are the angle in half
+// turns in [-1, 1), which sincospi takes. What is off: F by up to 2^-56 of a turn (w is a
+// 64-bit floating-point number), which counts p times: 2^-25 of a turn at p = 2^31; and,
+// at every position, the rounding of those 32 bits to fp32's 24: up to 2^-26 of a turn.
 //
 // Bound: HBM; every element is read and written once. A thread owns two 16-byte
 // pieces of a head row (with the half layout the two halves of its pairs) and goes
@@ -15,10 +16,11 @@
 // all of them. It loads the pieces of a batch of heads before it writes the first: in
 // and out may be the same memory, so the compiler cannot do that by itself. The heads
 // are split over threads only as far as filling the GPU needs.
-// Measured (12 + 12 heads x 32760 tokens x 128, bf16, 403 MB): 69 us = 5.8 TB/s with
-// batches of two heads, 74 with four (fewer threads fit), 90 without batches. fp32
-// (2 x 24 heads x 4680 x 64, 115 MB): 19 us = 6.0 TB/s with four, 20.2 with two:
-// 16 bytes hold half as many pairs, so angles and registers weigh half as much.
+// Measured on replay (12 + 12 heads x 32760 tokens x 128, bf16, 403 MB): 65.8 us = 6.1
+// TB/s with batches of two heads, 71 with four (fewer threads fit), 73 without batches.
+// fp32 (2 x 24 heads x 4680 x 64, 115 MB): 18.2 us = 6.3 TB/s with four, 19.6 with two,
+// 23.8 without: 16 bytes hold half as many pairs, so angles and registers weigh half as
+// much.
 #include <cmath>
 
 #include "kernels.h"
@@ -49,8 +51,8 @@ constexpr int kThreads = 128;
 
 // The plan lies among the kernel's parameters, from where lanes that read different
 // entries get them one after the other. Through an address whose origin the compiler does
-// not see they come like global memory (37762 tokens of 3 + 1 heads of 128: 25 us, 38 us
-// the other way).
+// not see they come like global memory (37762 tokens of 3 + 1 heads of 128: 14.1 us, 15.1
+// the other way; the case above 65.8 and 67.0).
 template <class E>
 __device__ __forceinline__ const E* as_memory(const E* p) {
   asm volatile("" : "+l"(p));
@@ -146,8 +148,8 @@ __device__ __forceinline__ void turn(float& x1, float& x2, float c, float s) {
 // two pieces of V channels at c0 and c1 (the second may be missing): with the half
 // layout channel c0 + e pairs with c1 + e, with the interleaved one neighbours within
 // a piece do (V = 1: c0 with c1 in both). Units behind rot_units copy.
-// (bf16: 64 registers, for the threads that hide the reads; fp32 spills with that: 21.2 us
-// instead of 19.7.)
+// (bf16: 64 registers, for the threads that hide the reads; fp32 is slower with that: 19.5
+// us instead of 18.2.)
 template <class T, int V, bool kInter>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 1) rotary_kernel(const __grid_constant__ RotaryParams p) {
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -249,9 +251,9 @@ int launch(RotaryParams& p, const tlsp_rotary_call& call, bool two, cudaStream_t
   p.batches[1] = two ? (int)ceil_div(p.t[1].heads, kBatch<T>) : 0;
   const int64_t rows = (int64_t)p.batch * p.tokens;
   // Enough threads to fill the GPU, but no more than that: each further split computes the
-  // angles once more (bf16, 37762 tokens of 3 + 1 heads: 15 us, 25 with 4096 threads an SM;
-  // the case above 69 us with 1536, 76 with 8192. fp32, the case above: 19.7 us with 1024,
-  // 20.7 with 768, 23.8 with 2048).
+  // angles once more (bf16, 37762 tokens of 3 + 1 heads: 14.1 us, 24.7 with 4096 threads an
+  // SM; the case above 65.8 us with 1536, 74.8 with 8192; 16381 tokens of 40 + 8 heads 66.3
+  // us, 78 with 768. fp32, the case above: 18.2 us with 1024, 19.2 with 768, 22.7 with 2048).
   const int64_t want = (int64_t)device_sm_count() * (sizeof(T) == 2 ? 1536 : 1024);
   const int64_t split = std::min<int64_t>(p.batches[0] + p.batches[1],
                                           std::max<int64_t>(1, ceil_div(want, rows * p.units)));
