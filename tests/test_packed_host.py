@@ -444,18 +444,18 @@ def test_merges_that_no_grid_holds(T, dtype):
 
 
 def test_plans_of_many_sequences_take_time_in_proportion(T):
-    """Single tokens by the ten thousand behind a prefix: four times as many take well below
-    sixteen times as long (the best of three each)."""
+    """Single tokens by the ten thousand behind a prefix: eight times as many take well below
+    sixty-four times as long (each the best of a few)."""
     import time
 
-    def seconds(n):
+    def seconds(n, times):
         q, kv = (ctypes.c_int32 * n)(*[1] * n), (ctypes.c_int32 * n)(*[5] * n)
         desc, data, best = T.PackedDesc(n, 16, 1, 64, 1, 1, 1), T.PackedPlanData(), 1e9
-        for _ in range(3):
+        for _ in range(times):
             start = time.perf_counter()
             assert T.lib().tlsp_packed_make_plan(ctypes.byref(desc), q, kv, None, None, 0,
                                                  ctypes.byref(data)) == T.TLSP_ERR_WORKSPACE
             best = min(best, time.perf_counter() - start)
         assert data.token_items == n
         return best
-    assert seconds(80000) < 9 * seconds(20000)
+    assert seconds(160000, 2) < 30 * seconds(20000, 5)
