@@ -638,7 +638,8 @@ class PackedPlan:
         self._made_on = torch.cuda.current_stream(device).cuda_stream
 
     def workspace(self) -> "Workspace":
-        """A workspace for calls with this plan (calls that overlap in time need one each)."""
+        """A workspace for calls with this plan (calls that overlap in time need one each), zeroed
+        on the current stream. Like the plan, kept until replays of graphs that use it are done."""
         return Workspace(None, nbytes=self.data.ws_bytes, device=self.device)
 
 
