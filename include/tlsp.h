@@ -371,13 +371,13 @@ typedef struct {
 
 /* O (and lse fp32 [q_rows, heads], natural log, if not NULL) of the packed
  * sequences of a plan without prefix. `items` is the device copy of the item
- * table (16-byte aligned), read in the order of the stream. scale multiplies q . k (0: 1/sqrt(d)). Rows of O
- * and lse behind the last sequence are not written. O, lse and ws share no
- * memory with an input or each other (O may lie among an input's heads or
- * channels, as another part of one tensor), nor O's rows and heads with each
- * other: TLSP_ERR_INVALID_ARG. ws: at least
- * plan->ws_bytes, zero-filled once before its first use; calls that may
- * overlap in time need workspaces of their own. */
+ * table (16-byte aligned), read in the order of the stream. scale multiplies
+ * q . k (0: 1/sqrt(d)); scale log2(e) must be finite. Rows of O and lse behind
+ * the last sequence are not written. O, lse and ws share no memory with an
+ * input or each other (O may lie among an input's heads or channels, as another
+ * part of one tensor), nor O's rows and heads with each other:
+ * TLSP_ERR_INVALID_ARG. ws: at least plan->ws_bytes, zero-filled once before its
+ * first use; calls that may overlap in time need workspaces of their own. */
 int tlsp_packed_attention(const tlsp_packed_plan* plan, const void* items, const tlsp_rows* Q,
                           const tlsp_rows* K, const tlsp_rows* V, const tlsp_rows* O, float* lse,
                           float scale, void* ws, size_t ws_bytes, void* stream);
